@@ -463,6 +463,145 @@ dca_status_t dca_kv_append_paged(const void* k_new, const void* v_new, void* Kpo
                                  int num_blocks, const int* t, int B, int Hkv, int D, int s,
                                  int c, float base, void* stream);
 
+/* The paged 4-bit cache.  A row of D keys or values of one kv head is cut into
+ * D/64 groups of 64; each keeps a bf16 offset (its least value), a bf16 scale
+ * (the smallest bf16 with 15 * scale >= greatest - least) and 64 codes
+ *     c = rint((x - offset) / scale) in 0 .. 15   (half to even)
+ * that stand for c * scale + offset, so a stored value is off by at most
+ * scale / 2: 4.5 bits a value against the 16 of the bf16 caches.  A group that
+ * holds an infinity or a NaN reads back as NaN.
+ * A pool is [num_blocks][Hkv][block_rows / 64][tile], a tile of
+ * dca_kv4_tile_bytes(D) = 72 * D bytes holding the keys and the values of 64
+ * rows of one kv head (block_rows a multiple of 64):
+ *     K codes   [64 keys][4 chunks][D/64 groups][2 words][4 bytes]
+ *     K params  [64 keys][D/64]            scale, offset (bf16 each)
+ *     V codes   [4][D/64 groups][8 words][16 keys][4 bytes]
+ *     V params  [64 keys][D/64]            scale, offset
+ * Word 2c + w of a group is word w of chunk c (K); word i holds the group's
+ * dims 8i .. 8i+7, lowest nibble first.  Keys are stored rotated at j mod s.
+ * Position p of sequence b lives in row p % block_rows of block
+ * block_table[b * max_blocks + p / block_rows].
+ * Returns 0 for unsupported D. */
+size_t dca_kv4_tile_bytes(int D);
+
+/* Append to a paged 4-bit cache: the next tokens of B sequences, packed.
+ * Sequence b's new tokens are rows cu_seqlens[b] .. cu_seqlens[b+1]-1 of k_new
+ * (UNROTATED) and v_new [T][Hkv][D] bf16 and go to positions t0[b], t0[b]+1, ..
+ * (one decoded token a sequence: cu_seqlens = 0 .. B; a prompt: its length at
+ * once).  A key is rotated at its position mod s and rounded once to bf16 (the
+ * value dca_kv_append stores), then quantised; other rows are untouched.  Both
+ * roundings are those of the exact result, so a cache does not depend on how
+ * its tokens were split into calls.
+ * cu_seqlens, t0: DEVICE int32 [B+1], [B].  A sequence whose span is not
+ * inside [0, T) or does not fit max_blocks * block_rows is skipped and
+ * reported by dca_sync_status (INVALID_ARG), as is a row whose table entry lies
+ * outside [0, num_blocks).  Rows of no sequence are ignored.
+ * Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+dca_status_t dca_kv4_append_paged(const void* k_new, const void* v_new, void* pool,
+                                  const int* block_table, int max_blocks, int block_rows,
+                                  int num_blocks, const int* cu_seqlens, const int* t0, int B,
+                                  int T, int Hkv, int D, int s, int c, float base, void* stream);
+
+/* Read rows of a paged 4-bit cache back as bf16: positions t0[b] .. t0[b]+n-1
+ * of sequence b (n = cu_seqlens[b+1] - cu_seqlens[b]), keys as stored (rotated)
+ * and values.  out_rows = 0: to packed rows cu_seqlens[b] .. of K, V
+ * [T][Hkv][D].  out_rows > 0: position p to row p of entry b of K, V
+ * [B][out_rows][Hkv][D], the bf16 caches of dca_attn_prefill_varlen_chunk and
+ * dca_attn_decode (a 4-bit prefix is read into a bf16 cache, extended by a
+ * chunk, and the chunk's rows are appended here).  Rows of K, V that belong to
+ * no position are untouched.  Offsets and table entries are checked as by
+ * dca_kv4_append_paged (with out_rows > 0 the span must fit out_rows too).
+ * Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+dca_status_t dca_kv4_read_paged(const void* pool, const int* block_table, int max_blocks,
+                                int block_rows, int num_blocks, const int* cu_seqlens,
+                                const int* t0, void* K, void* V, int B, int T, int Hkv, int D,
+                                int out_rows, void* stream);
+
+/* Workspace bytes of dca_attn_decode_kv4_paged for caches of Tcap = max_blocks *
+ * block_rows rows.  Returns 0 for unsupported arguments. */
+size_t dca_attn_decode_kv4_workspace(int B, int Hq, int Hkv, int D, int Tcap);
+
+/* dca_attn_decode over a paged 4-bit cache: q [B][Hq][D] bf16 UNROTATED at
+ * absolute index t[b] (device int32 [B]); positions 0 .. t[b] of the cache are
+ * valid, the new token's included.  O [B][Hq][D] bf16, LSE [B][Hq] fp32; s, c,
+ * base, scale as dca_attn_decode.  Rows past t[b] may hold anything.  The
+ * rotated query enters the scores with about 22 significant bits and the
+ * codes exactly; P times the value scale is rounded to bf16.  A t[b] outside
+ * the cache, or a table entry outside [0, num_blocks) that the sequence reads,
+ * is reported by dca_sync_status (INVALID_ARG) and that sequence's outputs
+ * are NaN.  Two calls that overlap on the GPU need a workspace each.
+ * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA. */
+dca_status_t dca_attn_decode_kv4_paged(const void* q, const void* pool, const int* block_table,
+                                       int max_blocks, int block_rows, int num_blocks,
+                                       const int* t, void* O, float* LSE, int B, int Hq, int Hkv,
+                                       int D, int s, int c, float base, float scale,
+                                       void* workspace, size_t ws_bytes, void* stream);
+
+/* A pool whose pages the page operations move: page p is the page_bytes =
+ * outer * (block_rows / unit_rows) * unit_bytes bytes at base + p * page_bytes,
+ * [outer][block_rows / unit_rows][unit_bytes]; a partial page is copied in
+ * units of unit_rows rows.  A bf16 pool [num_blocks][block_rows][Hkv][D] is
+ * {base, 2 * Hkv * D, 1, 1}; a 4-bit pool {base, 72 * D, Hkv, 64}. */
+typedef struct dca_page_pool {
+  void* base;        /* device, 16-byte aligned                 */
+  size_t unit_bytes; /* a multiple of 16                        */
+  int outer;         /* parts of a page                         */
+  int unit_rows;     /* rows of a unit; divides block_rows      */
+} dca_page_pool_t;
+
+/* Workspace bytes of dca_pages_remap and dca_pages_compact.  Returns 0 for
+ * unsupported arguments. */
+size_t dca_pages_workspace(int B, int max_blocks, int num_blocks);
+
+/* One step of the slots over paged pools: fork, share, reorder, cut, grow and
+ * free sequences without moving whole caches.  Slot b of the block table
+ * [B][max_blocks] holds old_len[b] rows in its first ceil(old_len[b] /
+ * block_rows) pages; refs [num_blocks] counts the entries that name a page (a
+ * caller may add to it to keep pages).  Afterwards slot b holds
+ *   - the first keep = min(old_len[src[b]], new_len[b]) rows of OLD slot src[b]
+ *     (src[b] = b: its own; another slot's: a fork or a beam's reordering;
+ *     -1: none), and
+ *   - pages for new_len[b] rows (0: the slot is freed).
+ * Full pages are shared.  The page that keep ends inside goes on being written
+ * to, so it must be the slot's own: if nothing else refers to it, the lowest
+ * slot that keeps it takes it as it is, and every other slot gets a new page
+ * with its rows copied, in all pools.  Pages that nobody refers to any more are
+ * free, in the same call.  New pages are the free ones of lowest index, slots
+ * in order, pages in order: the result depends on the arguments alone.
+ *   block_table_out, refs_out: the new state (unused entries -1); each may be
+ *     the array it replaces.  src, old_len, new_len: device int32 [B].
+ *   info: device int32 [2]: pages left free and pages copied.  When the free
+ *     pages do not suffice nothing changes (the outputs are the inputs) and
+ *     info[0] is minus the number of pages missing.
+ * A src, length or used table entry out of range, or a count below the number
+ * of entries that name its page, changes nothing either, sets info[0] to
+ * 2^31 - 1 and is reported by dca_sync_status (INVALID_ARG).
+ * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA. */
+dca_status_t dca_pages_remap(const int* src, const int* old_len, const int* new_len,
+                             const int* block_table, const int* refs, int* block_table_out,
+                             int* refs_out, int* info, int B, int max_blocks, int num_blocks,
+                             int block_rows, const dca_page_pool_t* pools, int n_pools,
+                             void* workspace, size_t ws_bytes, void* stream);
+
+/* Move all pages in use (refs > 0, n of them) to indexes 0 .. n-1, so that the
+ * rest of the pools can be given back or cut off: pages at n and above go, in
+ * ascending order, to the free indexes below n, in ascending order, and the
+ * other pages stay.  Slot b uses its first ceil(len[b] / block_rows) entries.
+ *   block_table_out, refs_out: the new state, each may be the array it
+ *     replaces; unused entries -1, counts of pages n and above 0.
+ *   moved: device int32 [num_blocks], the new index of every page in use (for
+ *     references the caller holds), -1 for a free one.
+ *   info: device int32 [2]: n and the number of pages moved.
+ * A length or used table entry out of range, a negative count, or an entry
+ * naming a page with none, changes nothing, sets info[0] to 2^31 - 1 (moved is
+ * the identity) and is reported by dca_sync_status (INVALID_ARG).
+ * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA. */
+dca_status_t dca_pages_compact(const int* len, const int* block_table, const int* refs,
+                               int* block_table_out, int* refs_out, int* moved, int* info, int B,
+                               int max_blocks, int num_blocks, int block_rows,
+                               const dca_page_pool_t* pools, int n_pools, void* workspace,
+                               size_t ws_bytes, void* stream);
+
 /* dca_attn_decode for callers that cannot allocate device memory (e.g. a
  * plugin inside a serving framework whose allocator owns the GPU's memory, or
  * a decode loop that must avoid cudaMalloc's implicit synchronisation).  Same

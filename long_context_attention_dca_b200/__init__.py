@@ -12,6 +12,7 @@ Build the library with ``python -m long_context_attention_dca_b200.build``.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -33,6 +34,9 @@ __all__ = [
     "dca_attn_prefill_host_workspace", "dca_attn_prefill_host",
     "dca_attn_decode_paged", "dca_kv_append_paged",
     "dca_attn_decode_workspace", "dca_attn_decode", "dca_attn_decode_noalloc", "dca_kv_append",
+    "dca_kv4_tile_bytes", "dca_kv4_append_paged", "dca_kv4_read_paged",
+    "dca_attn_decode_kv4_workspace", "dca_attn_decode_kv4_paged",
+    "dca_pages_workspace", "dca_pages_remap", "dca_pages_compact",
     "dca_debug_index_map", "dca_debug_wait_timeout",
     "dca_sync_status", "dca_last_error_string", "EXPORTED_SYMBOLS",
 ]
@@ -89,6 +93,16 @@ _SIGS = {
     "dca_kv_append": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _F, _P]),
     "dca_attn_decode_noalloc": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F,
                                      _F, _P]),
+    "dca_kv4_tile_bytes": (_Z, [_I]),
+    "dca_kv4_append_paged": (_I, [_P, _P, _P, _P, _I, _I, _I, _P, _P, _I, _I, _I, _I, _I, _I, _F,
+                                  _P]),
+    "dca_kv4_read_paged": (_I, [_P, _P, _I, _I, _I, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P]),
+    "dca_attn_decode_kv4_workspace": (_Z, [_I, _I, _I, _I, _I]),
+    "dca_attn_decode_kv4_paged": (_I, [_P, _P, _P, _I, _I, _I, _P, _P, _P, _I, _I, _I, _I, _I, _I,
+                                       _F, _F, _P, _Z, _P]),
+    "dca_pages_workspace": (_Z, [_I, _I, _I]),
+    "dca_pages_remap": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _I, _P, _Z, _P]),
+    "dca_pages_compact": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _I, _P, _Z, _P]),
     "dca_debug_index_map": (_I, [_I, _I, _I, _P, _P, _P, _P]),
     "dca_debug_wait_timeout": (_I, [_I, _P]),
     "dca_sync_status": (_I, [_P]),
@@ -538,6 +552,232 @@ def dca_kv_append_paged(k_new, v_new, Kpool, Vpool, block_table, t, s, c, base=1
                                      _ptr(block_table), block_table.shape[1], Kpool.shape[1],
                                      Kpool.shape[0], _ptr(t), B, Hkv, D, s, c, base,
                                      _stream(k_new)))
+
+
+def _on_device(first: torch.Tensor, *others):
+    """The context that makes `first`'s device current for the launches; the
+    other tensors (or None) must be on it too."""
+    dev = first.device
+    for t in others:
+        if t is not None and t.device != dev:
+            raise DcaError(1, f"tensors on {dev} and {t.device}")
+    if dev.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(dev)
+
+
+def dca_kv4_tile_bytes(D: int) -> int:
+    return int(lib().dca_kv4_tile_bytes(D))
+
+
+def _kv4_pool(pool, D):
+    """(num_blocks, Hkv, block_rows) of a 4-bit pool uint8 [num_blocks, Hkv,
+    block_rows / 64, dca_kv4_tile_bytes(D)]."""
+    _need(pool, "pool", torch.uint8, 4)
+    num_blocks, Hkv, tiles, nbytes = pool.shape
+    if nbytes != 72 * D:
+        raise DcaError(1, f"pool tiles of {nbytes} bytes do not hold heads of {D}")
+    return num_blocks, Hkv, tiles * 64
+
+
+def _kv4_rows(cu_seqlens, t0, block_table):
+    """B of a packed call over a block table."""
+    _need(block_table, "block_table", torch.int32, 2)
+    _need(cu_seqlens, "cu_seqlens", torch.int32, 1)
+    _need(t0, "t0", torch.int32, 1)
+    B = block_table.shape[0]
+    if cu_seqlens.numel() != B + 1 or t0.numel() != B:
+        raise DcaError(1, f"cu_seqlens and t0 must have {B + 1} and {B} entries, got "
+                          f"{cu_seqlens.numel()} and {t0.numel()}")
+    return B
+
+
+def dca_kv4_append_paged(k_new, v_new, pool, block_table, cu_seqlens, t0, s, c, base=10000.0):
+    """Rotate, quantise and store packed new tokens in a paged 4-bit cache, in
+    place.  k_new, v_new [T, Hkv, D] bf16; pool uint8 [num_blocks, Hkv,
+    block_rows / 64, dca_kv4_tile_bytes(D)]; block_table int32 [B, max_blocks],
+    cu_seqlens int32 [B+1], t0 int32 [B] on the device."""
+    _need(k_new, "k_new", torch.bfloat16, 3)
+    _need(v_new, "v_new", torch.bfloat16, 3)
+    T, Hkv, D = k_new.shape
+    num_blocks, pool_heads, block_rows = _kv4_pool(pool, D)
+    if v_new.shape != k_new.shape or pool_heads != Hkv:
+        raise DcaError(1, "k_new, v_new and pool disagree on rows or heads")
+    B = _kv4_rows(cu_seqlens, t0, block_table)
+    with _on_device(k_new, v_new, pool, block_table, cu_seqlens, t0):
+        _check(lib().dca_kv4_append_paged(
+            _ptr(k_new), _ptr(v_new), _ptr(pool), _ptr(block_table), block_table.shape[1],
+            block_rows, num_blocks, _ptr(cu_seqlens), _ptr(t0), B, T, Hkv, D, s, c, base,
+            _stream(k_new)))
+
+
+def dca_kv4_read_paged(pool, block_table, cu_seqlens, t0, T, D, K=None, V=None):
+    """Rows of a paged 4-bit cache as bf16: (K, V) [T, Hkv, D], sequence b's
+    positions t0[b], t0[b]+1, .. at rows cu_seqlens[b] .. cu_seqlens[b+1]-1.
+    With K, V [B, rows, Hkv, D] given, position p goes to row p of entry b."""
+    num_blocks, Hkv, block_rows = _kv4_pool(pool, D)
+    B = _kv4_rows(cu_seqlens, t0, block_table)
+    if (K is None) != (V is None):
+        raise DcaError(1, "K and V are given together or not at all")
+    if K is None:
+        K = torch.empty((T, Hkv, D), dtype=torch.bfloat16, device=pool.device)
+        V = torch.empty_like(K)
+    _need(K, "K", torch.bfloat16, K.dim())
+    _need(V, "V", torch.bfloat16, K.dim())
+    shape = (T, Hkv, D) if K.dim() == 3 else (B, K.shape[1], Hkv, D)
+    if tuple(K.shape) != shape or tuple(V.shape) != shape:
+        raise DcaError(1, f"K and V must be {shape}, got {tuple(K.shape)} and {tuple(V.shape)}")
+    with _on_device(pool, block_table, cu_seqlens, t0, K, V):
+        _check(lib().dca_kv4_read_paged(
+            _ptr(pool), _ptr(block_table), block_table.shape[1], block_rows, num_blocks,
+            _ptr(cu_seqlens), _ptr(t0), _ptr(K), _ptr(V), B, T, Hkv, D,
+            0 if K.dim() == 3 else K.shape[1], _stream(pool)))
+    return K, V
+
+
+def dca_attn_decode_kv4_workspace(B: int, Hq: int, Hkv: int, D: int, Tcap: int) -> int:
+    return int(lib().dca_attn_decode_kv4_workspace(B, Hq, Hkv, D, Tcap))
+
+
+def dca_attn_decode_kv4_paged(q, pool, block_table, t, s, c, base=10000.0, scale=0.0,
+                              workspace=None, O=None, LSE=None):
+    """DCA decode over a paged 4-bit cache: q [B, Hq, D] bf16 unrotated, pool
+    and block_table as dca_kv4_append_paged, t int32 [B] on the device.
+    Returns (O [B, Hq, D] bf16, LSE [B, Hq] fp32)."""
+    _need(q, "q", torch.bfloat16, 3)
+    _need(block_table, "block_table", torch.int32, 2)
+    _need(t, "t", torch.int32, 1)
+    B, Hq, D = q.shape
+    num_blocks, Hkv, block_rows = _kv4_pool(pool, D)
+    max_blocks = block_table.shape[1]
+    if block_table.shape[0] != B or t.numel() != B:
+        raise DcaError(1, f"block_table and t must have {B} rows")
+    O = torch.empty_like(q) if O is None else O
+    LSE = torch.empty((B, Hq), dtype=torch.float32, device=q.device) if LSE is None else LSE
+    _need(O, "O", torch.bfloat16, 3)
+    _need(LSE, "LSE", torch.float32, 2)
+    if O.shape != q.shape or tuple(LSE.shape) != (B, Hq):
+        raise DcaError(1, "O must have the shape of q and LSE [B, Hq]")
+    if workspace is None:
+        workspace = _workspace(dca_attn_decode_kv4_workspace(B, Hq, Hkv, D,
+                                                             max_blocks * block_rows), q.device)
+    with _on_device(q, pool, block_table, t, O, LSE, workspace):
+        _check(lib().dca_attn_decode_kv4_paged(
+            _ptr(q), _ptr(pool), _ptr(block_table), max_blocks, block_rows, num_blocks, _ptr(t),
+            _ptr(O), _ptr(LSE), B, Hq, Hkv, D, s, c, base, scale, _ptr(workspace),
+            workspace.numel(), _stream(q)))
+    return O, LSE
+
+
+class _PagePool(ctypes.Structure):
+    _fields_ = [("base", _P), ("unit_bytes", _Z), ("outer", _I), ("unit_rows", _I)]
+
+
+def _page_pools(pools, num_blocks, block_rows, device):
+    """The descriptors of pools with pages of block_rows rows: bf16 [num_blocks,
+    block_rows, Hkv, D], 4-bit uint8 [num_blocks, Hkv, block_rows / 64, tile],
+    given one by one or stacked in one 5-d tensor."""
+    if isinstance(pools, torch.Tensor):
+        stacked = pools.dim() == 5
+        given = [(pools, pools.shape[0] if stacked else 1, 1 if stacked else 0)]
+    else:
+        given = [(p, 1, 0) for p in pools]
+    out = (_PagePool * max(1, sum(n for _, n, _ in given)))()
+    at = 0
+    for p, n, lead in given:
+        if not isinstance(p, torch.Tensor) or not p.is_cuda or p.device != device:
+            raise DcaError(1, f"pools must be tensors on {device}")
+        if p.dim() != 4 + lead or not p.is_contiguous() or p.shape[lead] != num_blocks:
+            raise DcaError(1, f"a pool must be contiguous with {num_blocks} pages, got "
+                              f"{tuple(p.shape)}")
+        a, b, width = p.shape[lead + 1:]
+        if p.dtype == torch.uint8 and b * 64 == block_rows:
+            desc = (width, a, 64)
+        elif p.dtype == torch.bfloat16 and a == block_rows:
+            desc = (2 * b * width, 1, 1)
+        else:
+            raise DcaError(1, f"a pool of {p.dtype} {tuple(p.shape)} has no pages of "
+                              f"{block_rows} rows")
+        base, step = p.data_ptr(), p.stride(0) * p.element_size()
+        for i in range(n):
+            out[at] = (base + i * step, *desc)
+            at += 1
+    return out, at
+
+
+def _page_state(block_table, refs, lens, outs):
+    """Check the page state and allocate the outputs that were not given."""
+    _need(block_table, "block_table", torch.int32, 2)
+    _need(refs, "refs", torch.int32, 1)
+    B = block_table.shape[0]
+    for name, x in lens:
+        _need(x, name, torch.int32, 1)
+        if x.numel() != B:
+            raise DcaError(1, f"{name} must have {B} entries, got {x.numel()}")
+    got = []
+    for name, x, like in outs:
+        x = torch.empty_like(like) if x is None else x
+        _need(x, name, torch.int32, like.dim())
+        if x.shape != like.shape:
+            raise DcaError(1, f"{name} must be {tuple(like.shape)}, got {tuple(x.shape)}")
+        got.append(x)
+    return got
+
+
+def dca_pages_workspace(B: int, max_blocks: int, num_blocks: int) -> int:
+    return int(lib().dca_pages_workspace(B, max_blocks, num_blocks))
+
+
+def dca_pages_remap(src, old_len, new_len, block_table, refs, pools, block_rows, workspace=None,
+                    block_table_out=None, refs_out=None, info=None):
+    """One step of the slots over paged pools (fork, share, reorder, cut, grow,
+    free; see dca.h).  src, old_len, new_len int32 [B]; block_table int32 [B,
+    max_blocks]; refs int32 [num_blocks]; pools: tensors whose partial pages are
+    copied, one by one or stacked.  Returns (block_table, refs, info), new
+    tensors unless given (a given one may be the one it replaces)."""
+    table_out, counts_out = _page_state(
+        block_table, refs, (("src", src), ("old_len", old_len), ("new_len", new_len)),
+        (("block_table_out", block_table_out, block_table), ("refs_out", refs_out, refs)))
+    if info is None:
+        info = torch.empty(2, dtype=torch.int32, device=refs.device)
+    _need(info, "info", torch.int32, 1)
+    B, max_blocks = block_table.shape
+    num_blocks = refs.numel()
+    desc, n = _page_pools(pools, num_blocks, block_rows, refs.device)
+    if workspace is None:
+        workspace = _workspace(dca_pages_workspace(B, max_blocks, num_blocks), refs.device)
+    with _on_device(refs, src, old_len, new_len, block_table, table_out, counts_out, info,
+                    workspace):
+        _check(lib().dca_pages_remap(
+            _ptr(src), _ptr(old_len), _ptr(new_len), _ptr(block_table), _ptr(refs),
+            _ptr(table_out), _ptr(counts_out), _ptr(info), B, max_blocks, num_blocks, block_rows,
+            ctypes.byref(desc), n, _ptr(workspace), workspace.numel(), _stream(refs)))
+    return table_out, counts_out, info
+
+
+def dca_pages_compact(lens, block_table, refs, pools, block_rows, workspace=None,
+                      block_table_out=None, refs_out=None, moved=None, info=None):
+    """Move all pages in use to the front of their pools (see dca.h).  lens int32
+    [B], the rest as dca_pages_remap.  Returns (block_table, refs, moved, info)
+    with moved int32 [num_blocks], the new index of every page (-1: free)."""
+    table_out, counts_out, moved = _page_state(
+        block_table, refs, (("lens", lens),),
+        (("block_table_out", block_table_out, block_table), ("refs_out", refs_out, refs),
+         ("moved", moved, refs)))
+    if info is None:
+        info = torch.empty(2, dtype=torch.int32, device=refs.device)
+    _need(info, "info", torch.int32, 1)
+    B, max_blocks = block_table.shape
+    num_blocks = refs.numel()
+    desc, n = _page_pools(pools, num_blocks, block_rows, refs.device)
+    if workspace is None:
+        workspace = _workspace(dca_pages_workspace(B, max_blocks, num_blocks), refs.device)
+    with _on_device(refs, lens, block_table, table_out, counts_out, moved, info, workspace):
+        _check(lib().dca_pages_compact(
+            _ptr(lens), _ptr(block_table), _ptr(refs), _ptr(table_out), _ptr(counts_out),
+            _ptr(moved), _ptr(info), B, max_blocks, num_blocks, block_rows, ctypes.byref(desc), n,
+            _ptr(workspace), workspace.numel(), _stream(refs)))
+    return table_out, counts_out, moved, info
 
 
 def dca_attn_decode_noalloc(q, Kcache, Vcache, t, s, c, base=10000.0, scale=0.0, O=None,

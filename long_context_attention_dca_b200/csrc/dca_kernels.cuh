@@ -140,6 +140,49 @@ cudaError_t launch_decode_paged(const void* q, const void* Kpool, const void* Vp
                                 int Hkv, int D, int s, int c, float base, float scale,
                                 void* workspace, cudaStream_t stream);
 
+// Paged 4-bit cache (kv4.cuh): pool of num_blocks pages of [Hkv][block_rows / 64]
+// tiles through block_table [B][max_blocks].  Append and read take packed rows
+// (cu device [B+1], T rows) at absolute indices t0[b] + local row; read writes
+// packed rows, or with out_rows > 0 rows of [B][out_rows][Hkv][D].
+cudaError_t launch_kv4_append(const void* k_new, const void* v_new, void* pool,
+                              const int* block_table, int max_blocks, int block_rows,
+                              int num_blocks, const int* cu, const int* t0, int B, int T, int Hkv,
+                              int D, int s, float base, cudaStream_t stream);
+cudaError_t launch_kv4_read(const void* pool, const int* block_table, int max_blocks,
+                            int block_rows, int num_blocks, const int* cu, const int* t0,
+                            void* K, void* V, int B, int T, int Hkv, int D, int out_rows,
+                            cudaStream_t stream);
+// Decode over it (cap = max_blocks * block_rows).
+size_t kv4_decode_workspace_bytes(int B, int Hq, int Hkv, int D, long long cap);
+cudaError_t launch_kv4_decode(const void* q, const void* pool, const int* block_table,
+                              int max_blocks, int block_rows, int num_blocks, const int* t,
+                              void* O, float* LSE, int B, int Hq, int Hkv, int D, int s, int c,
+                              float base, float scale, void* workspace, cudaStream_t stream);
+
+// Pools whose pages move together: page = [outer][block_rows / unit_rows][unit_bytes].
+struct PoolDesc {
+  unsigned char* base;
+  long long unit_bytes;
+  int outer, unit_rows;
+  int chunks, items;  // per part and per page (filled by the launcher)
+};
+constexpr int kMaxPools = 256;
+struct PoolList {
+  long long items;  // of one page over all pools (filled by the launcher)
+  int n;
+  PoolDesc p[kMaxPools];
+};
+size_t pages_workspace_bytes(int B, int max_blocks, int num_blocks);
+cudaError_t launch_pages_remap(const int* src, const int* old_len, const int* new_len,
+                               const int* table_in, int* table_out, const int* refs_in,
+                               int* refs_out, int* info, int B, int max_blocks, int num_blocks,
+                               int block_rows, PoolList& pools, void* workspace,
+                               cudaStream_t stream);
+cudaError_t launch_pages_compact(const int* len, const int* table_in, int* table_out,
+                                 const int* refs_in, int* refs_out, int* moved, int* info, int B,
+                                 int max_blocks, int num_blocks, int block_rows, PoolList& pools,
+                                 void* workspace, cudaStream_t stream);
+
 cudaError_t launch_wait_timeout(int deadline_us, cudaStream_t stream);
 
 cudaError_t launch_index_map(int L, int s, int c, int* qpos, int* kpos, signed char* piece,

@@ -10,3 +10,7 @@
 #include "attn_decode.cu"
 #include "decode_noalloc.cu"
 #include "prefill_host.cu"
+#include "kv4_cache.cu"
+#include "attn_decode_kv4.cu"
+#include "pages.cu"
+#include "kv4_api.cu"

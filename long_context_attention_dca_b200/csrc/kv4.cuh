@@ -1,0 +1,92 @@
+// The 4-bit key/value cache: its tile, its quantiser and the fp64 rotation
+// angles its kernels share.
+//
+// A cache row (one token, one kv head) of D values is cut into D/64 groups of
+// 64.  A group keeps a bf16 offset (its least value, which is a bf16 already),
+// a bf16 scale (the smallest bf16 with 15 * scale >= greatest - least) and 64
+// codes c in 0 .. 15:
+//     c = rint((x - offset) / scale)  (half to even),  value = c * scale + offset,
+// so |x - value| <= scale / 2 for every finite input.  A group that holds an
+// infinity or a NaN keeps NaN parameters and reads back as NaN.
+//
+// 64 rows of one kv head form a tile of 72 * D bytes, contiguous, so that one
+// bulk copy brings everything a warp of the decode kernel needs:
+//     K codes   [64 keys][4 chunks][D/64][2 words]    row-wise: chunk t holds
+//               words 2t, 2t+1 of every group, 16 bytes at D = 128
+//     K params  [64 keys][D/64]    scale in the low, offset in the high half
+//     V codes   [4][D/64][8 words][16 keys]           transposed per 16 keys
+//     V params  [64 keys][D/64]
+// Word i of a group holds its dims 8i .. 8i+7, lowest nibble first; a word
+// belongs to one token, so an append writes whole words.  The two orders make
+// every shared-memory read of the decode kernel a conflict-free 16-byte load
+// of exactly the lane's own MMA fragments.
+// A page is [Hkv][block_rows / 64] tiles.
+#pragma once
+
+#include <cmath>
+
+#include "dca_common.cuh"
+
+namespace dca {
+namespace kv4 {
+
+constexpr int kTileKeys = 64;
+constexpr int kGroup = 64;
+
+template <int D>
+struct Tile {
+  static constexpr int kGroups = D / kGroup;
+  static constexpr int kCodeBytes = kTileKeys * D / 2;
+  static constexpr int kParamBytes = kTileKeys * kGroups * 4;
+  static constexpr int kKCodes = 0;
+  static constexpr int kKParams = kCodeBytes;
+  static constexpr int kVCodes = kKParams + kParamBytes;
+  static constexpr int kVParams = kVCodes + kCodeBytes;
+  static constexpr int kBytes = kVParams + kParamBytes;
+  // byte offset of word i of group g of key r (0 .. 63)
+  __host__ __device__ static constexpr int k_word(int r, int g, int i) {
+    return kKCodes + (((r * 4 + (i >> 1)) * kGroups + g) * 2 + (i & 1)) * 4;
+  }
+  __host__ __device__ static constexpr int v_word(int r, int g, int i) {
+    return kVCodes + ((((r >> 4) * kGroups + g) * 8 + i) * 16 + (r & 15)) * 4;
+  }
+  __host__ __device__ static constexpr int k_param(int r, int g) {
+    return kKParams + (r * kGroups + g) * 4;
+  }
+  __host__ __device__ static constexpr int v_param(int r, int g) {
+    return kVParams + (r * kGroups + g) * 4;
+  }
+};
+inline size_t tile_bytes(int D) { return (size_t)72 * D; }
+
+// RoPE frequencies base^(-2k/D) in fp64, computed once on the host and passed
+// by value (the device never evaluates a power).
+struct Theta {
+  double v[64];
+};
+inline Theta make_theta(int D, float base) {
+  Theta t;
+  for (int k = 0; k < 64; ++k)
+    t.v[k] = k < D / 2 ? std::pow((double)base, -2.0 * k / D) : 0.0;
+  return t;
+}
+
+// Where a paged cache lives: pool of num_blocks pages, block_table [B][max_blocks].
+struct Pages {
+  uint8_t* pool;
+  const int* table;
+  int max_blocks, block_rows, num_blocks, Hkv;
+};
+// The tile of position pos of sequence b and kv head h; null when the table
+// names no page of the pool.
+template <int D>
+__device__ __forceinline__ uint8_t* tile_of(const Pages& pg, int b, int pos, int h) {
+  const int blk = __ldg(pg.table + (size_t)b * pg.max_blocks + pos / pg.block_rows);
+  if (blk < 0 || blk >= pg.num_blocks) return nullptr;
+  const int tpb = pg.block_rows / kTileKeys;
+  return pg.pool + (((size_t)blk * pg.Hkv + h) * tpb + (pos % pg.block_rows) / kTileKeys) *
+                       Tile<D>::kBytes;
+}
+
+}  // namespace kv4
+}  // namespace dca

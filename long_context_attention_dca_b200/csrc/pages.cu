@@ -1,0 +1,483 @@
+// Pages of a cache: which slot holds which page, and the moves that follow.
+//
+// A pool is num_blocks pages; slot b of the block table [B][max_blocks] lists
+// the pages of its sequence; refs[p] counts the table entries that name page p
+// (plus whatever the caller added to keep a page).  Both operations are
+// functions of that state with one result: pages are taken lowest index first,
+// slots served in order, so neither the launch shape nor the order of atomics
+// shows in the outputs.
+//
+// Each runs as two kernels.  The plan is integer work over B * max_blocks
+// entries and num_blocks counts with a handful of dependent phases: one
+// cluster of 8 CTAs, whose hardware barrier separates the phases, holds it in
+// one launch.  The copies move the bytes, a chunk a block at a time, from a
+// list whose length stays on the device; they are bound by memory bandwidth.
+#include "dca_common.cuh"
+#include "dca_kernels.cuh"
+
+namespace dca {
+namespace pages {
+
+constexpr int kCluster = 8;
+constexpr int kPlanThreads = 1024;
+constexpr int kAll = kCluster * kPlanThreads;
+constexpr int kNone = 0x7FFFFFFF;
+
+__device__ __forceinline__ void cluster_barrier() {
+  __threadfence();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ int pages_of(int n, int R) {
+  return (int)(((long long)n + R - 1) / R);
+}
+
+// Exclusive prefix sum of one value a thread over the block; `total` gets the sum.
+__device__ __forceinline__ int block_scan(int v, int* warp_sums, int& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int x = v;
+#pragma unroll
+  for (int sh = 1; sh < 32; sh <<= 1) {
+    const int y = __shfl_up_sync(0xFFFFFFFFu, x, sh);
+    if (lane >= sh) x += y;
+  }
+  if (lane == 31) warp_sums[warp] = x;
+  __syncthreads();
+  if (warp == 0) {
+    int w = warp_sums[lane];
+#pragma unroll
+    for (int sh = 1; sh < 32; sh <<= 1) {
+      const int y = __shfl_up_sync(0xFFFFFFFFu, w, sh);
+      if (lane >= sh) w += y;
+    }
+    warp_sums[lane] = w;
+  }
+  __syncthreads();
+  const int before = (warp ? warp_sums[warp - 1] : 0) + x - v;
+  total = warp_sums[31];
+  __syncthreads();
+  return before;
+}
+
+// Part of 0 .. n-1 that CTA `rank` scans: contiguous, so that a rank within the
+// part plus the parts before it is a rank in the whole.
+struct Part {
+  int begin, end;
+};
+__device__ __forceinline__ Part part_of(int n, int rank) {
+  const int per = (int)(((long long)n + kCluster - 1) / kCluster);
+  const long long a = (long long)per * rank;
+  return Part{(int)min(a, (long long)n), (int)min(a + per, (long long)n)};
+}
+
+struct Work {  // workspace, all int32
+  int* head;    // [64]: 0 faults, 1 copies; 8.. per-CTA sums
+  int* count;   // [num_blocks] references while the plan runs
+  int* owner;   // [num_blocks] slot that keeps a partial page
+  int* list;    // [num_blocks] free pages or holes, ascending
+  int* from;    // [max(num_blocks, B)] copy list: source page
+  int* to;      //                       target page
+  int* rows;    //                       rows to copy
+  int* table;   // [B * max_blocks] the table as it came
+  int* slots;   // [3][B] full pages kept, rows of the partial one, first new page
+};
+constexpr int kHead = 64;
+
+size_t work_ints(int B, int max_blocks, int num_blocks) {
+  const size_t m = (size_t)(num_blocks > B ? num_blocks : B);
+  return kHead + 3 * (size_t)num_blocks + 3 * m + (size_t)B * max_blocks + 3 * (size_t)B;
+}
+Work carve(void* ws, int B, int max_blocks, int num_blocks) {
+  const size_t m = (size_t)(num_blocks > B ? num_blocks : B);
+  Work w;
+  int* p = static_cast<int*>(ws);
+  w.head = p;
+  p += kHead;
+  w.count = p;
+  p += num_blocks;
+  w.owner = p;
+  p += num_blocks;
+  w.list = p;
+  p += num_blocks;
+  w.from = p;
+  p += m;
+  w.to = p;
+  p += m;
+  w.rows = p;
+  p += m;
+  w.table = p;
+  p += (size_t)B * max_blocks;
+  w.slots = p;
+  return w;
+}
+
+// New slot b holds the first keep = min(old_len[src[b]], new_len[b]) rows of old
+// slot src[b] (none for -1) and pages for new_len[b] rows.  Full pages are
+// shared.  A partial last page goes to the lowest slot that wants it unless it
+// is still held elsewhere; every other slot gets a copy of its rows.
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads, 1) remap_plan(
+    const int* __restrict__ src, const int* __restrict__ old_len,
+    const int* __restrict__ new_len, const int* table_in, int* table_out, const int* refs_in,
+    int* refs_out, int* __restrict__ info, int B, int max_blocks, int num_blocks, int R,
+    Work w) {
+  __shared__ int sums[32];
+  __shared__ int carry;
+  const int rank = blockIdx.x, tid = threadIdx.x;
+  const int gid = rank * kPlanThreads + tid;
+  const long long entries = (long long)B * max_blocks;
+  const long long cap = (long long)max_blocks * R;
+  if (rank == 0 && tid < kHead) w.head[tid] = 0;
+  for (int p = gid; p < num_blocks; p += kAll) {
+    w.count[p] = refs_in[p];
+    w.owner[p] = kNone;
+  }
+  for (long long e = gid; e < entries; e += kAll) w.table[e] = table_in[e];
+  cluster_barrier();
+
+  // drop what the slots hold; a fault anywhere refuses the whole call
+  bool bad = false;
+  for (int b = gid; b < B; b += kAll) {
+    const int f = src[b], n = new_len[b], o = old_len[b];
+    const bool ok = f >= -1 && f < B && n >= 0 && n <= cap && o >= 0 && o <= cap;
+    bad |= !ok;
+    int keep = 0;
+    if (ok && f >= 0) keep = max(0, min(old_len[f], n));
+    w.slots[b] = keep / R;
+    w.slots[B + b] = keep % R;
+  }
+  for (long long e = gid; e < entries; e += kAll) {
+    const int b = (int)(e / max_blocks), i = (int)(e % max_blocks);
+    const int o = old_len[b];
+    if (o < 0 || o > cap || i >= pages_of(o, R)) continue;
+    const int p = w.table[e];
+    if (p < 0 || p >= num_blocks) bad = true;
+    else if (atomicSub(w.count + p, 1) <= 0) bad = true;  // fewer references than entries
+  }
+  for (int p = gid; p < num_blocks; p += kAll) bad |= refs_in[p] < 0;
+  if (bad) atomicExch(w.head, 1);
+  cluster_barrier();
+  const bool fault = __ldcg(w.head) != 0;
+
+  // full pages are shared by every slot that keeps them
+  if (!fault) {
+    for (long long e = gid; e < entries; e += kAll) {
+      const int b = (int)(e / max_blocks), i = (int)(e % max_blocks);
+      if (i < __ldcg(w.slots + b)) {
+        const int f = src[b];
+        atomicAdd(w.count + __ldcg(w.table + (size_t)f * max_blocks + i), 1);
+      }
+    }
+  }
+  cluster_barrier();
+  // partial pages that nobody holds any more go to the lowest slot
+  if (!fault) {
+    for (int b = gid; b < B; b += kAll) {
+      if (__ldcg(w.slots + B + b) == 0) continue;
+      const int p = __ldcg(w.table + (size_t)src[b] * max_blocks + __ldcg(w.slots + b));
+      if (__ldcg(w.count + p) == 0) atomicMin(w.owner + p, b);
+    }
+  }
+  cluster_barrier();
+
+  // free pages in ascending order, each CTA ranking its own part
+  const Part mine = part_of(num_blocks, rank);
+  int local = 0;
+  for (int p = mine.begin + tid; p < mine.end; p += kPlanThreads)
+    local += __ldcg(w.count + p) == 0 && __ldcg(w.owner + p) == kNone;
+  int part_free;
+  block_scan(local, sums, part_free);
+  if (tid == 0) w.head[8 + rank] = part_free;
+  // new pages of the slots, in order; every CTA needs only the total and rank
+  // 0 writes where each slot starts
+  if (rank == 0) {
+    if (tid == 0) carry = 0;
+    __syncthreads();
+    for (int b0 = 0; b0 < B; b0 += kPlanThreads) {
+      const int b = b0 + tid;
+      int need = 0;
+      if (b < B && !fault) {
+        const int full = __ldcg(w.slots + b), rest = __ldcg(w.slots + B + b);
+        bool stays = false;
+        if (rest) {
+          const int p = __ldcg(w.table + (size_t)src[b] * max_blocks + full);
+          stays = __ldcg(w.owner + p) == b;
+        }
+        need = pages_of(new_len[b], R) - full - (stays ? 1 : 0);
+      }
+      int total;
+      const int before = block_scan(need, sums, total);
+      if (b < B) w.slots[2 * B + b] = carry + before;
+      __syncthreads();
+      if (tid == 0) carry = (int)min((long long)carry + total, (long long)kNone);
+      __syncthreads();
+    }
+    if (tid == 0) w.head[2] = carry;
+  }
+  cluster_barrier();
+
+  int before = 0, free_all = 0;
+  for (int r = 0; r < kCluster; ++r) {
+    const int n = __ldcg(w.head + 8 + r);
+    if (r < rank) before += n;
+    free_all += n;
+  }
+  const int need_all = __ldcg(w.head + 2);
+  if (fault || need_all > free_all) {  // refused: the state as it came
+    for (long long e = gid; e < entries; e += kAll) table_out[e] = __ldcg(w.table + e);
+    if (refs_out != refs_in)
+      for (int p = gid; p < num_blocks; p += kAll) refs_out[p] = refs_in[p];
+    if (gid == 0) {
+      info[0] = fault ? kNone : -(need_all - free_all);
+      info[1] = 0;
+      if (fault) report_error(kDevBadArg, 209);
+    }
+    return;
+  }
+  for (int p0 = mine.begin; p0 < mine.end; p0 += kPlanThreads) {
+    const int p = p0 + tid;
+    int n = 0, free = 0;
+    if (p < mine.end) {
+      n = __ldcg(w.count + p);
+      const bool kept = __ldcg(w.owner + p) != kNone;
+      if (kept) n = 1;
+      free = n == 0;
+    }
+    int total;
+    const int at = before + block_scan(free, sums, total);
+    if (p < mine.end) {
+      if (free) {
+        w.list[at] = p;
+        n = at < need_all;
+      }
+      refs_out[p] = n;
+    }
+    before += total;
+  }
+  cluster_barrier();
+
+  for (long long e = gid; e < entries; e += kAll) {
+    const int b = (int)(e / max_blocks), i = (int)(e % max_blocks);
+    const int full = __ldcg(w.slots + b), rest = __ldcg(w.slots + B + b);
+    const int n = pages_of(new_len[b], R);
+    int page = -1;
+    if (i < n) {
+      const int* row = w.table + (size_t)max(src[b], 0) * max_blocks;
+      if (i < full) {
+        page = __ldcg(row + i);
+      } else {
+        const int tail = rest ? __ldcg(row + full) : -1;
+        const bool stays = rest && __ldcg(w.owner + tail) == b;
+        if (i == full && stays) {
+          page = tail;
+        } else {
+          page = __ldcg(w.list + __ldcg(w.slots + 2 * B + b) + i - full - (stays ? 1 : 0));
+          if (i == full && rest) {
+            const int k = atomicAdd(w.head + 1, 1);
+            w.from[k] = tail;
+            w.to[k] = page;
+            w.rows[k] = rest;
+          }
+        }
+      }
+    }
+    table_out[e] = page;
+  }
+  cluster_barrier();
+  if (gid == 0) {
+    info[0] = free_all - need_all;
+    info[1] = __ldcg(w.head + 1);
+  }
+}
+
+// Pages in use (refs > 0) with an index of n or more, n their number, move to
+// the free indexes below n, both in ascending order.
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads, 1) compact_plan(
+    const int* __restrict__ len, const int* table_in, int* table_out, const int* refs_in,
+    int* refs_out, int* __restrict__ moved, int* __restrict__ info, int B, int max_blocks,
+    int num_blocks, int R, Work w) {
+  __shared__ int sums[32];
+  const int rank = blockIdx.x, tid = threadIdx.x;
+  const int gid = rank * kPlanThreads + tid;
+  const long long entries = (long long)B * max_blocks;
+  const long long cap = (long long)max_blocks * R;
+  const Part mine = part_of(num_blocks, rank);
+  if (rank == 0 && tid < 8) w.head[tid] = 0;
+  bool bad = false;
+  int local = 0;
+  for (int p = mine.begin + tid; p < mine.end; p += kPlanThreads) {
+    const int n = refs_in[p];
+    w.count[p] = n;
+    local += n > 0;
+    bad |= n < 0;
+  }
+  int part_live;
+  block_scan(local, sums, part_live);
+  if (tid == 0) w.head[8 + rank] = part_live;
+  for (long long e = gid; e < entries; e += kAll) {
+    const int b = (int)(e / max_blocks), i = (int)(e % max_blocks);
+    const int n = len[b];
+    w.table[e] = table_in[e];
+    if (n < 0 || n > cap) {
+      bad = true;
+    } else if (i < pages_of(n, R)) {
+      const int p = table_in[e];
+      if (p < 0 || p >= num_blocks || refs_in[p] <= 0) bad = true;
+    }
+  }
+  if (max_blocks > 0)
+    for (int b = gid; b < B; b += kAll) bad |= len[b] < 0 || len[b] > cap;
+  cluster_barrier();
+  if (bad) atomicExch(w.head, 1);
+  int before = 0, live = 0;
+  for (int r = 0; r < kCluster; ++r) {
+    const int n = __ldcg(w.head + 8 + r);
+    if (r < rank) before += n;
+    live += n;
+  }
+  // how many of the pages below n are in use
+  local = 0;
+  for (int p = mine.begin + tid; p < min(mine.end, live); p += kPlanThreads)
+    local += w.count[p] > 0;
+  int part_low;
+  block_scan(local, sums, part_low);
+  if (tid == 0) w.head[16 + rank] = part_low;
+  cluster_barrier();
+  if (__ldcg(w.head)) {
+    for (long long e = gid; e < entries; e += kAll) table_out[e] = __ldcg(w.table + e);
+    if (refs_out != refs_in)
+      for (int p = gid; p < num_blocks; p += kAll) refs_out[p] = refs_in[p];
+    for (int p = gid; p < num_blocks; p += kAll) moved[p] = p;
+    if (gid == 0) {
+      info[0] = kNone;
+      info[1] = 0;
+      report_error(kDevBadArg, 210);
+    }
+    return;
+  }
+  int low = 0;
+  for (int r = 0; r < kCluster; ++r) low += __ldcg(w.head + 16 + r);
+  for (int p0 = mine.begin; p0 < mine.end; p0 += kPlanThreads) {
+    const int p = p0 + tid;
+    const int used = p < mine.end && w.count[p] > 0;
+    int total;
+    const int at = before + block_scan(used, sums, total);  // pages in use below p
+    if (p < mine.end) {
+      if (used && p >= live) w.from[at - low] = p;
+      if (!used && p < live) w.to[p - at] = p;
+    }
+    before += total;
+  }
+  cluster_barrier();
+  const int moves = live - low;
+  for (int p = gid; p < num_blocks; p += kAll) {
+    const int n = __ldcg(w.count + p);
+    moved[p] = n > 0 && p < live ? p : -1;
+    refs_out[p] = p < live ? n : 0;  // holes are filled below
+  }
+  cluster_barrier();
+  for (int k = gid; k < moves; k += kAll) {
+    const int a = __ldcg(w.from + k), z = __ldcg(w.to + k);
+    moved[a] = z;
+    refs_out[z] = __ldcg(w.count + a);
+    w.rows[k] = R;
+  }
+  cluster_barrier();
+  for (long long e = gid; e < entries; e += kAll) {
+    const int b = (int)(e / max_blocks), i = (int)(e % max_blocks);
+    table_out[e] = i < pages_of(len[b], R) ? __ldcg(moved + __ldcg(w.table + e)) : -1;
+  }
+  if (gid == 0) {
+    info[0] = live;
+    info[1] = moves;
+    w.head[1] = moves;
+  }
+}
+
+// Copies of the list, in every pool: the first ceil(rows / unit_rows) units of
+// each outer part of a page.  A work item is one chunk of one part; items are
+// numbered over the longest possible copy and the ones past a short copy's end
+// do nothing.
+constexpr int kChunk = 32 << 10;
+constexpr int kCopyThreads = 256;
+
+__global__ void __launch_bounds__(kCopyThreads) copy_pages(const __grid_constant__ PoolList pools,
+                                                           int R, Work w) {
+  const int n = __ldcg(w.head + 1);
+  const long long items = (long long)n * pools.items;
+  for (long long it = blockIdx.x; it < items; it += gridDim.x) {
+    const int k = (int)(it / pools.items);
+    int rem = (int)(it % pools.items), j = 0;
+    while (rem >= pools.p[j].items) rem -= pools.p[j++].items;
+    const PoolDesc d = pools.p[j];
+    const int part = rem / d.chunks, chunk = rem % d.chunks;
+    const int units = (__ldcg(w.rows + k) + d.unit_rows - 1) / d.unit_rows;
+    const long long bytes = (long long)units * d.unit_bytes;
+    const long long at = (long long)chunk * kChunk;
+    if (at >= bytes) continue;
+    const long long part_bytes = (long long)(R / d.unit_rows) * d.unit_bytes;
+    const size_t a = ((size_t)__ldcg(w.from + k) * d.outer + part) * part_bytes + at;
+    const size_t z = ((size_t)__ldcg(w.to + k) * d.outer + part) * part_bytes + at;
+    const int words = (int)(min(bytes - at, (long long)kChunk) / 16);
+    const uint4* from = reinterpret_cast<const uint4*>(d.base + a);
+    uint4* to = reinterpret_cast<uint4*>(d.base + z);
+    constexpr int kPer = kChunk / 16 / kCopyThreads;
+    uint4 v[kPer];
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) {
+      const int x = threadIdx.x + u * kCopyThreads;
+      if (x < words) v[u] = __ldcs(from + x);
+    }
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) {
+      const int x = threadIdx.x + u * kCopyThreads;
+      if (x < words) __stcs(to + x, v[u]);
+    }
+  }
+}
+
+cudaError_t launch_copies(PoolList& pools, int R, const Work& w, cudaStream_t stream) {
+  pools.items = 0;
+  for (int j = 0; j < pools.n; ++j) {
+    PoolDesc& d = pools.p[j];
+    const long long part = (long long)(R / d.unit_rows) * d.unit_bytes;
+    d.chunks = (int)((part + kChunk - 1) / kChunk);
+    d.items = d.outer * d.chunks;
+    pools.items += d.items;
+  }
+  if (pools.items == 0) return cudaSuccess;
+  copy_pages<<<148 * 6, kCopyThreads, 0, stream>>>(pools, R, w);
+  return cudaGetLastError();
+}
+
+}  // namespace pages
+
+size_t pages_workspace_bytes(int B, int max_blocks, int num_blocks) {
+  return pages::work_ints(B, max_blocks, num_blocks) * sizeof(int);
+}
+
+cudaError_t launch_pages_remap(const int* src, const int* old_len, const int* new_len,
+                               const int* table_in, int* table_out, const int* refs_in,
+                               int* refs_out, int* info, int B, int max_blocks, int num_blocks,
+                               int block_rows, PoolList& pools, void* workspace,
+                               cudaStream_t stream) {
+  const pages::Work w = pages::carve(workspace, B, max_blocks, num_blocks);
+  pages::remap_plan<<<pages::kCluster, pages::kPlanThreads, 0, stream>>>(
+      src, old_len, new_len, table_in, table_out, refs_in, refs_out, info, B, max_blocks,
+      num_blocks, block_rows, w);
+  cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? pages::launch_copies(pools, block_rows, w, stream) : e;
+}
+
+cudaError_t launch_pages_compact(const int* len, const int* table_in, int* table_out,
+                                 const int* refs_in, int* refs_out, int* moved, int* info, int B,
+                                 int max_blocks, int num_blocks, int block_rows, PoolList& pools,
+                                 void* workspace, cudaStream_t stream) {
+  const pages::Work w = pages::carve(workspace, B, max_blocks, num_blocks);
+  pages::compact_plan<<<pages::kCluster, pages::kPlanThreads, 0, stream>>>(
+      len, table_in, table_out, refs_in, refs_out, moved, info, B, max_blocks, num_blocks,
+      block_rows, w);
+  cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? pages::launch_copies(pools, block_rows, w, stream) : e;
+}
+
+}  // namespace dca
