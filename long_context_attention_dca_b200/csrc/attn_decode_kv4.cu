@@ -9,56 +9,83 @@
 // pre-scaled by 1/16), so eight codes cost four logic operations and a shift.
 // q is kept as an fp16 high part and remainder (normalised per head by a power
 // of two), about 22 significant bits.  For the values,
-//     O = sum_j p_j (c_j - 8) scale_j + sum_j p_j (offset_j + 8 scale_j):
-// centred codes are exact in bf16 and keep the sums near the size of the
-// result; p_j scale_j is rounded to bf16 (as P is in the bf16 decode) and the
-// second sum stays in fp32 outside the matrix product.
+//     O = sum_j (p_j scale_j) c_j + sum_j p_j offset_j,
+// again on the bare codes, with p_j scale_j rounded to fp16 after a
+// normalisation by the largest scale of the 64-key tile (a power of two), so
+// that any range of scales fits; the second sum stays in fp32 outside the
+// matrix product.  A tile's product is formed from zero and then added to O in
+// fp32: the codes are not centred, so a long sum inside the tensor core, which
+// truncates, would drift by more than the result can bear.
 //
 // Kernel 1, one CTA per (share of the cache, kv head, group of <= 8 query
-// heads, sequence): a producer warp brings whole 64-key tiles (K and V codes
-// and their parameters, 72 * D contiguous bytes) with one bulk copy each into a
-// ring; four consumer warps take tiles in turn, so that the running maximum, its
-// shuffles and the rescaling of O are paid once per 64 keys of a warp.  The
-// sequence's tiles are shared out evenly on the device from t[b], whatever the
-// cache's capacity.  Kernel 2 merges the shares.
+// heads, sequence): four warps take the share's 64-key tiles in turn, each
+// fetching its own tiles (K part and V part, 36 * D contiguous bytes each, one
+// bulk copy) through a small ring, so that the running maximum, its shuffles
+// and the update of O are paid once per 64 keys of a warp.  The sequence's
+// tiles are shared out evenly on the device from t[b], whatever the cache's
+// capacity.  Kernel 2 merges the shares.
 #include "dca_common.cuh"
 #include "dca_index.cuh"
 #include "dca_kernels.cuh"
 #include "kv4.cuh"
+#include "softmax_sm100.cuh"
 
 namespace dca {
 namespace kv4 {
 
-constexpr int kHeads = 8;        // query heads per CTA (MMA N)
-constexpr int kWarps = 4;        // consumer warps
-constexpr int kDecodeThreads = (kWarps + 1) * 32;
-constexpr int kStages = 6;
+constexpr int kHeads = 8;   // query heads per CTA (MMA N)
+constexpr int kWarps = 4;   // per CTA, each with a ring of its own
+constexpr int kRing = 3;    // half tiles (K or V part) of a ring
+constexpr int kDecodeThreads = kWarps * 32;
+constexpr int kCtasPerSm = 3;
+constexpr int kMany = 2;    // 16-key steps whose score products run interleaved
+constexpr int kMaxTiles = 512;  // of a CTA's share, so that their places fit in shared memory
 
-// CTAs wanted in flight over the whole call: three fit an SM, and shares of
-// unequal sequences even out over a few waves.
-constexpr int kWantCtas = 148 * 3 * 2;
-inline int decode_shares(int B, int Hq, int Hkv, long long cap) {
-  if (B == 0) return 1;
-  const int G = Hq / Hkv;
-  const long long units = (long long)B * Hkv * ((G + kHeads - 1) / kHeads);
-  const long long tiles = (cap + kTileKeys - 1) / kTileKeys;
-  long long n = (kWantCtas + units - 1) / units;
-  if (n > tiles) n = tiles;
-  if (n > 256) n = 256;
-  return n < 1 ? 1 : (int)n;
+// Work.  A unit is a (sequence, kv head, group of <= 8 query heads).  The tiles
+// of all units, one unit after another, are cut into equal shares, a CTA each,
+// so neither unequal sequences nor few of them leave SMs idle.  Every unit
+// counts kSetup tiles besides its own, before them, for what it costs to begin
+// one (rotating the queries, the first fetch, the merge).  A share may hold the
+// end of one unit and the beginning of the next; each piece gives a partial
+// result.  Share c of unit U writes slot U + c: along the line of tiles each new
+// piece raises one of the two, so no slot is used twice.
+constexpr int kSetup = 12;
+struct Split {
+  long long tiles;  // of all units
+  long long shares;
+};
+__host__ __device__ inline long long share_begin(const Split& sp, long long c) {
+  return c * sp.tiles / sp.shares;
+}
+// The share that holds tile g.
+__device__ __forceinline__ long long share_of(const Split& sp, long long g) {
+  return ((g + 1) * sp.shares - 1) / sp.tiles;
+}
+inline int head_groups(int Hq, int Hkv) { return (Hq / Hkv + kHeads - 1) / kHeads; }
+// Most shares of a call (the grid): all SMs once, or more where a share would
+// pass kMaxTiles.  The kernels use fewer when that leaves a share under one
+// tile a warp.
+inline long long decode_shares(int B, int Hq, int Hkv, long long cap) {
+  const long long tiles = (long long)B * Hkv * head_groups(Hq, Hkv) *
+                          ((cap + kTileKeys - 1) / kTileKeys + kSetup);
+  const long long need = (tiles + kMaxTiles - 1) / kMaxTiles;
+  const long long most = need > 148 * kCtasPerSm ? need : 148 * kCtasPerSm;
+  return most < tiles ? most : (tiles > 0 ? tiles : 1);
 }
 
 template <int D>
 struct DecodeSmem {
-  static constexpr int kRing = kStages * Tile<D>::kBytes;
+  static constexpr int kHalf = Tile<D>::kBytes / 2;
+  static constexpr int kRings = kWarps * kRing * kHalf;
   // [piece][hi, lo][group][head][word] x 16 bytes of query fragments
   static constexpr int kQ = 3 * 2 * (D / 64) * kHeads * 8 * 16;
   static constexpr int kCs = 3 * (D / 2) * 8;          // cos, sin
   static constexpr int kSums = 3 * kHeads * (D / 64) * 4;  // sum of q per group
   static constexpr int kF = kHeads * 4;
-  static constexpr int kBars = 2 * kStages * 8 + 16;  // + abort, page and copy words
-  static constexpr int kTotal = 128 + kRing + kQ + kCs + kSums + kF + kBars;
-  static_assert(kWarps * kHeads * (D + 2) * 4 <= kRing, "merge area");
+  static constexpr int kBars = kWarps * kRing * 8 + 16;  // + abort and page words
+  static constexpr int kPlaces = kMaxTiles * 4;  // pool tile of every tile of the share
+  static constexpr int kTotal = kRings + kQ + kCs + kSums + kF + kBars + kPlaces;
+  static_assert(kWarps * kHeads * (D + 2) * 4 <= kRings, "merge area");
 };
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
@@ -68,139 +95,198 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
       ::"r"(dst), "l"(src), "r"(bytes), "r"(bar)
       : "memory");
 }
-__device__ __forceinline__ void lds128(uint32_t (&r)[4], uint32_t a) {
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(a));
+// m16n8k16 on fp16, fp32 accumulate; volatile, which keeps the products in the
+// order written (two independent ones in turn): left to itself the compiler
+// gathers all loads of a tile first and spills.
+__device__ __forceinline__ void mma_codes(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                          uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void lds64(uint32_t& x, uint32_t& y, uint32_t a) {
-  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(x), "=r"(y) : "r"(a));
+// The first product of a sum (C = 0).
+__device__ __forceinline__ void mma_codes_first(float (&d)[4], const uint32_t (&a)[4],
+                                                uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-  uint32_t x;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(x) : "r"(a));
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
+  uint32_t d;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// Greater of either bf16 half (NaN only against NaN).
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 m = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&a),
+                                   *reinterpret_cast<const __nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&m);
+}
+
+__device__ __forceinline__ int tiles_of(int t, long long cap) {
+  return t >= 0 && t < cap ? t / kTileKeys + 1 : 0;
+}
+// The same with its setup, on the line of shares; 0 for a bad position.
+__device__ __forceinline__ int span_of(int t, long long cap) {
+  const int n = tiles_of(t, cap);
+  return n ? n + kSetup : 0;
+}
+// Spans of sequences 0 .. n-1 (units of one sequence counted once), by the block.
+__device__ __forceinline__ long long spans_before(const int* t, int n, long long cap,
+                                                  long long* sums) {
+  long long x = 0;
+  for (int b = threadIdx.x; b < n; b += blockDim.x) x += span_of(__ldg(t + b), cap);
+#pragma unroll
+  for (int sh = 16; sh >= 1; sh >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, sh);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = x;
+  __syncthreads();
+  x = 0;
+  for (int w = 0; w < (int)(blockDim.x >> 5); ++w) x += sums[w];
   return x;
 }
-
-// Shares of a sequence of n_tiles tiles: tiles per share; share sp holds tiles
-// sp * per .. (sp + 1) * per - 1.
-__device__ __forceinline__ int tiles_per_share(int n_tiles, int shares) {
-  return (n_tiles + shares - 1) / shares;
-}
-
-// Codes of one nibble position as bf16 pairs c - 8 (exact).
-__device__ __forceinline__ uint32_t centred(uint32_t w) {
-  const uint32_t v = (w & 0x000F000Fu) | 0x43004300u;  // 128 + c
-  const uint32_t bias = 0x43084308u;                   // 136
-  const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v),
-                                   *reinterpret_cast<const __nv_bfloat162*>(&bias));
-  return *reinterpret_cast<const uint32_t*>(&d);
+__device__ __forceinline__ Split make_split(long long tiles, long long most) {
+  long long n = tiles / kWarps;
+  n = n < most ? n : most;
+  return Split{tiles, n > 0 ? n : 1};
 }
 
 template <int D>
-__global__ void __launch_bounds__(kDecodeThreads, 3) decode_kernel(
+__global__ void __launch_bounds__(kDecodeThreads, kCtasPerSm) decode_kernel(
     const __nv_bfloat16* __restrict__ q, Pages pg, const int* __restrict__ t,
-    float* __restrict__ Opart, float* __restrict__ MLpart, int Hq, int s, int c, float scale_log2,
-    int shares, int n_hg, const __grid_constant__ Theta theta) {
+    float* __restrict__ Opart, float2* __restrict__ MLpart, int B, int Hq, int s, int c,
+    float scale_log2, int n_hg, const __grid_constant__ Theta theta) {
   using TL = Tile<D>;
   using SM = DecodeSmem<D>;
   constexpr int kGr = TL::kGroups;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 127) & ~(uintptr_t)127);
-  const uint32_t ring = smem_u32(smem);
-  uint8_t* qf = smem + SM::kRing;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ long long sums[kWarps];
+  uint8_t* qf = smem + SM::kRings;
   float2* cs = reinterpret_cast<float2*>(qf + SM::kQ);
   float* qsum = reinterpret_cast<float*>(qf + SM::kQ + SM::kCs);  // [piece][head][group]
   float* qexp = qsum + 3 * kHeads * kGr;                          // [head]
   uint8_t* bars = reinterpret_cast<uint8_t*>(qexp + kHeads);
-  const uint32_t full0 = smem_u32(bars), empty0 = full0 + kStages * 8;
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + 2 * kStages * 8);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + kWarps * kRing * 8);
   volatile int* bad_page = abort_flag + 1;
-  volatile int* issued = abort_flag + 2;  // copies started
+  uint32_t* places = reinterpret_cast<uint32_t*>(bars + SM::kBars);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int sp = blockIdx.x;
-  const int hg = blockIdx.y % n_hg, hk = blockIdx.y / n_hg, b = blockIdx.z;
-  const int G = Hq / pg.Hkv;
-  const int tb = __ldg(t + b);
-  if (tb < 0 || tb >= pg.max_blocks * pg.block_rows) {
-    if (tid == 0 && sp == 0 && blockIdx.y == 0) report_error(kDevBadArg, 207);
-    return;
+  const int G = Hq / pg.Hkv, per_seq = pg.Hkv * n_hg;
+  const int tpb = pg.block_rows / kTileKeys;
+  const long long cap = (long long)pg.max_blocks * pg.block_rows;
+  const Split split = make_split(spans_before(t, B, cap, sums) * per_seq, gridDim.x);
+  if (blockIdx.x == 0) {  // positions outside the cache: reported, no work
+    for (int b = tid; b < B; b += kDecodeThreads)
+      if (tiles_of(__ldg(t + b), cap) == 0) report_error(kDevBadArg, 207);
   }
-  const int all_tiles = tb / kTileKeys + 1;
-  const int per = tiles_per_share(all_tiles, shares);
-  const int tile0 = sp * per;
-  if (tile0 >= all_tiles) return;
-  const int n_tiles = min(per, all_tiles - tile0);
-  const int h_base = hk * G + hg * kHeads;
-  const int n_heads = min(kHeads, G - hg * kHeads);
-
-  if (tid == 0) {
-    for (int i = 0; i < kStages; ++i) {
-      mbar_init(full0 + 8 * i, 1);
-      mbar_init(empty0 + 8 * i, 1);
+  if (blockIdx.x >= split.shares || split.tiles == 0) return;
+  long long at = share_begin(split, blockIdx.x);
+  const long long end = share_begin(split, blockIdx.x + 1);
+  // the sequence at the share's begin, and where that sequence begins (every
+  // warp looks, 32 sequences at a time)
+  int b = 0;
+  long long b_at = 0;
+  for (;; b += 32) {
+    const long long mine =
+        b + lane < B ? (long long)span_of(__ldg(t + b + lane), cap) * per_seq : 0;
+    long long sum = mine;
+#pragma unroll
+    for (int sh = 1; sh < 32; sh <<= 1) {
+      const long long y = __shfl_up_sync(0xFFFFFFFFu, sum, sh);
+      if (lane >= sh) sum += y;
     }
+    const unsigned past = __ballot_sync(0xFFFFFFFFu, at < b_at + sum);
+    if (past) {
+      const int k = __ffs(past) - 1;
+      b_at += __shfl_sync(0xFFFFFFFFu, sum - mine, k);
+      b += k;
+      break;
+    }
+    b_at += __shfl_sync(0xFFFFFFFFu, sum, 31);
+  }
+  if (tid == 0) {
     *abort_flag = 0;
-    *bad_page = 0;
-    *issued = 0;
+    for (int i = 0; i < kWarps * kRing; ++i) mbar_init(smem_u32(bars) + 8 * i, 1);
     fence_barrier_init();
   }
-  __syncthreads();
+  // This warp's ring: the K and V parts of its tiles pass in turn through its
+  // buffers; a part is fetched as soon as the one kRing before it is read.
+  const uint8_t* ring = smem + warp * kRing * SM::kHalf;
+  const uint32_t full0 = smem_u32(bars) + warp * kRing * 8;
+  int buf = 0, phase = 0;
 
-  if (warp == kWarps) {
-    // ---------------- producer ----------------
-    const int tpb = pg.block_rows / kTileKeys;
-    for (int it0 = 0; it0 < n_tiles; it0 += 32) {
-      // the pages of the next 32 tiles, one lookup a lane
-      const int mine = tile0 + it0 + lane;
-      const uint8_t* src = nullptr;
-      if (it0 + lane < n_tiles) {
-        int blk = __ldg(pg.table + (size_t)b * pg.max_blocks + mine / tpb);
-        if (blk < 0 || blk >= pg.num_blocks) {  // reported; the outputs become NaN
-          report_error(kDevBadArg, 208);
-          *bad_page = 1;
-          blk = 0;
-        }
-        src = pg.pool + (((size_t)blk * pg.Hkv + hk) * tpb + mine % tpb) * TL::kBytes;
-      }
-      const int n = min(32, n_tiles - it0);
-      bool ok = true;
-      for (int j = 0; j < n && ok; ++j) {
-        const int it = it0 + j, st = it % kStages;
-        const uint8_t* from = reinterpret_cast<const uint8_t*>(
-            __shfl_sync(0xFFFFFFFFu, (unsigned long long)src, j));
-        if (it >= kStages)
-          ok = warp_wait(empty0 + 8 * st, ((it / kStages) + 1) & 1, abort_flag, 401);
-        if (ok && lane == 0) {
-          mbar_arrive_expect_tx(full0 + 8 * st, TL::kBytes);
-          bulk_load(ring + st * TL::kBytes, from, TL::kBytes, full0 + 8 * st);
-          *issued = it + 1;
-        }
-      }
-      if (!ok) break;
-    }
+  while (at < end) {
+  const int tb = __ldg(t + b), all_tiles = tiles_of(tb, cap), span = all_tiles + kSetup;
+  const int unit = (int)((at - b_at) / span);
+  const long long unit_at = b_at + (long long)unit * span;
+  const int tile0 = max(0, (int)(at - unit_at) - kSetup);
+  const int tile1 = max(0, (int)(min(end - unit_at, (long long)span)) - kSetup);
+  const int n_tiles = tile1 - tile0;
+  at = unit_at + span < end ? unit_at + span : end;
+  const int seq = b;
+  if (at == b_at + (long long)span * per_seq) {
+    b_at = at;
+    do ++b;
+    while (b < B && tiles_of(__ldg(t + b), cap) == 0);
   }
+  if (n_tiles == 0) continue;  // the share ends inside the unit's setup
+  const int hg = unit % n_hg, hk = unit / n_hg;
+  const int h_base = hk * G + hg * kHeads;
+  const int n_heads = min(kHeads, G - hg * kHeads);
+  if (tid == 0) *bad_page = 0;
+  __syncthreads();
+  for (int i = tid; i < n_tiles; i += kDecodeThreads) {
+    const int tile = tile0 + i;
+    int blk = __ldg(pg.table + (size_t)seq * pg.max_blocks + tile / tpb);
+    if ((unsigned)blk >= (unsigned)pg.num_blocks) {
+      report_error(kDevBadArg, 208);  // the outputs become NaN
+      *bad_page = 1;
+      blk = 0;
+    }
+    places[i] = (uint32_t)(((size_t)blk * pg.Hkv + hk) * tpb + tile % tpb);
+  }
+  __syncthreads();
+  const int parts = n_tiles > warp ? 2 * ((n_tiles - warp + kWarps - 1) / kWarps) : 0;
+  // lane 0: fetch part i of this warp's tiles into buffer `to`
+  auto fetch = [&](int i, int to) {
+    const uint8_t* src = pg.pool + (size_t)places[warp + (i >> 1) * kWarps] * TL::kBytes +
+                         (i & 1) * SM::kHalf;
+    const uint32_t bar = full0 + 8 * to;
+    mbar_arrive_expect_tx(bar, SM::kHalf);
+    bulk_load(smem_u32(ring) + to * SM::kHalf, src, SM::kHalf, bar);
+  };
+  if (lane == 0)
+    for (int i = 0, to = buf; i < min(parts, kRing); ++i, to = to == kRing - 1 ? 0 : to + 1)
+      fetch(i, to);
 
   // ---------------- queries: three rotations, fragments, group sums ----------------
-  if (warp < kWarps) {
+  {
     const int im = tb % s;
+#pragma unroll 1
     for (int x = tid; x < 3 * (D / 2); x += kWarps * 32) {
       const int p = x / (D / 2), k = x % (D / 2);
-      constexpr double kTwoPi = 6.283185307179586476925286766559;
-      const double a = (double)query_pos_for_piece(p, im, s, c) * theta.v[k];
-      float sf, cf;
-      sincosf((float)fma(-rint(a * (1.0 / kTwoPi)), kTwoPi, a), &sf, &cf);
-      cs[x] = make_float2(cf, sf);
+      double cd, sd;
+      sincos64((double)query_pos_for_piece(p, im, s, c) * theta.v[k], cd, sd);
+      cs[x] = make_float2((float)cd, (float)sd);
     }
-    asm volatile("bar.sync 1, 128;" ::: "memory");
+    __syncthreads();
     constexpr int kPairs = D / 64;  // (k, k + D/2) pairs a lane owns of a head
+#pragma unroll 1
     for (int hh = warp; hh < kHeads; hh += kWarps) {
       float x0[kPairs], x1[kPairs], big = 0.f;
 #pragma unroll
       for (int u = 0; u < kPairs; ++u) {
         x0[u] = x1[u] = 0.f;
         if (hh < n_heads) {
-          const __nv_bfloat16* row = q + ((size_t)b * Hq + h_base + hh) * D + lane + 32 * u;
+          const __nv_bfloat16* row = q + ((size_t)seq * Hq + h_base + hh) * D + lane + 32 * u;
           x0[u] = __bfloat162float(row[0]) * scale_log2;
           x1[u] = __bfloat162float(row[D / 2]) * scale_log2;
         }
@@ -211,7 +297,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 3) decode_kernel(
       // every rotated value times 2^-e stays below 2^13
       const int e = big > 0.f ? (int)(__float_as_uint(big) >> 23) - 127 - 12 : 0;
       const float down = ldexpf(1.f, -(e / 2)), down2 = ldexpf(1.f, -(e - e / 2));
-#pragma unroll
+#pragma unroll 1
       for (int p = 0; p < 3; ++p) {
         float sum[2] = {0.f, 0.f};
 #pragma unroll
@@ -238,18 +324,20 @@ __global__ void __launch_bounds__(kDecodeThreads, 3) decode_kernel(
         for (int sh = 16; sh >= 1; sh >>= 1)
 #pragma unroll
           for (int g = 0; g < kGr; ++g) sum[g] += __shfl_xor_sync(~0u, sum[g], sh);
-        if (lane < kGr) qsum[(p * kHeads + hh) * kGr + lane] = lane == 0 ? sum[0] : sum[1];
+        // in the units of the code products
+        const float unit = down * down2 * 5.9604644775390625e-8f;  // 2^-24
+        if (lane < kGr) qsum[(p * kHeads + hh) * kGr + lane] = (lane == 0 ? sum[0] : sum[1]) * unit;
       }
       if (lane == 0) qexp[hh] = ldexpf(1.f, e + 24);
     }
-    asm volatile("bar.sync 1, 128;" ::: "memory");
+    __syncthreads();
   }
 
   const int g = lane >> 2, t4 = lane & 3;
   float m_run[2] = {-INFINITY, -INFINITY};  // heads 2 t4, 2 t4 + 1
   float l_run[2] = {0.f, 0.f};
-  float off[kGr][2];                        // sum of p (offset + 8 scale), by group
-  float o[kGr * 4][4];
+  float off[kGr][2];                        // sum of p * offset, by group
+  float o[kGr * 4][4];                      // times 2^-24; rows g + 8 times 16 besides
 #pragma unroll
   for (int i = 0; i < kGr * 4; ++i)
 #pragma unroll
@@ -257,118 +345,139 @@ __global__ void __launch_bounds__(kDecodeThreads, 3) decode_kernel(
 #pragma unroll
   for (int i = 0; i < kGr; ++i) off[i][0] = off[i][1] = 0.f;
 
-  if (warp < kWarps) {
-    // ---------------- consumers ----------------
-    const int ci = tb / s;
+  {
+    // ---------------- tiles ----------------
     const float F[2] = {qexp[2 * t4], qexp[2 * t4 + 1]};
-    int cur = -1;
-    uint32_t qh[kGr][2][4], ql[kGr][2][4];
-    float qs[kGr][2];
+    // first keys of the query's own chunk and of the one before
+    const int own0 = tb - tb % s, prev0 = own0 - s;
     const int kr = 4 * (g >> 1) + (g & 1);  // MMA row g holds key kr, row g + 8 key kr + 2
+    int part = 0;
+    auto next_part = [&]() {  // the part just read is free: fetch another in its place
+      __syncwarp();
+      if (lane == 0 && part + kRing < parts) fetch(part + kRing, buf);
+      ++part;
+      if (++buf == kRing) {
+        buf = 0;
+        phase ^= 1;
+      }
+    };
+#pragma unroll 1
     for (int it = warp; it < n_tiles; it += kWarps) {
-      const int st = it % kStages;
-      if (!warp_wait(full0 + 8 * st, (it / kStages) & 1, abort_flag, 402)) break;
-      const uint32_t tile = ring + st * TL::kBytes;
+      if (!warp_wait(full0 + 8 * buf, phase, abort_flag, 402)) break;
       const int j0 = (tile0 + it) * kTileKeys;
       const int j1 = min(j0 + kTileKeys - 1, tb);  // last valid key of the tile
-      float x[4][4];  // [16-key step][(kr, head 0), (kr, head 1), (kr + 2, ..), ..]
-      // pieces of the tile, nearest first; distances of 2 and more are one piece
-      const int dlo = min(ci - j1 / s, 2), dhi = min(ci - j0 / s, 2);
+      // scores over F: [16-key step][(kr, head 0), (kr, head 1), (kr + 2, ..), ..]
+      float x[4][4];
+#pragma unroll
+      for (int sub = 0; sub < 4; ++sub)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[sub][e] = 0.f;
+      // Scores of piece p, whose keys of the tile are p0 .. p1 - 1; in a tile of
+      // several pieces the other keys take part with parameters of 0.
+      auto scores = [&](auto several, int p, int p0, int p1) {
+        // the same codes again for the next piece: an offset that the compiler
+        // cannot follow keeps it from holding them all in registers meanwhile
+        uint32_t place = buf * SM::kHalf;
+        asm volatile("" : "+r"(place));
+        const uint8_t* codes = ring + place;
+#pragma unroll
+        for (int gr = 0; gr < kGr; ++gr) {
+          // the lane's two words of this group, high part and remainder
+          const uint4* qa = reinterpret_cast<const uint4*>(qf) +
+                            (((p * 2) * kGr + gr) * kHeads + g) * 8 + 2 * t4;
+          const uint4 h[2] = {qa[0], qa[1]};
+          const uint4 l[2] = {qa[kGr * kHeads * 8], qa[kGr * kHeads * 8 + 1]};
+          const float qs0 = qsum[(p * kHeads + 2 * t4) * kGr + gr];
+          const float qs1 = qsum[(p * kHeads + 2 * t4 + 1) * kGr + gr];
+#pragma unroll
+          for (int pair = 0; pair < 4; pair += kMany) {  // 16-key steps, interleaved
+            uint2 wa[kMany], wb[kMany];
+            uint32_t pa[kMany], pb[kMany];
+            float acc[kMany][4];
+#pragma unroll
+            for (int n = 0; n < kMany; ++n) {
+              const int r0 = (pair + n) * 16 + kr;
+              const uint8_t* ka = codes + TL::k_word(0, gr, 0) + r0 * (D / 2) + t4 * (D / 8);
+              const uint8_t* kp = codes + TL::k_param(0, gr) + r0 * (kGr * 4);
+              wa[n] = *reinterpret_cast<const uint2*>(ka);
+              wb[n] = *reinterpret_cast<const uint2*>(ka + D);
+              pa[n] = *reinterpret_cast<const uint32_t*>(kp);
+              pb[n] = *reinterpret_cast<const uint32_t*>(kp + kGr * 8);
+              if (several) {
+                if (r0 < p0 || r0 >= p1) pa[n] = 0u;
+                if (r0 + 2 < p0 || r0 + 2 >= p1) pb[n] = 0u;
+              }
+            }
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+              uint32_t u[kMany], v[kMany];
+#pragma unroll
+              for (int n = 0; n < kMany; ++n) {
+                u[n] = w ? wa[n].y : wa[n].x;
+                v[n] = w ? wb[n].y : wb[n].x;
+              }
+#pragma unroll
+              for (int half = 0; half < 2; ++half) {
+                uint32_t a[kMany][4];
+#pragma unroll
+                for (int n = 0; n < kMany; ++n) {
+                  const uint32_t uu = u[n] >> (8 * half), vv = v[n] >> (8 * half);
+                  a[n][0] = uu & 0x000F000Fu;
+                  a[n][1] = vv & 0x000F000Fu;
+                  a[n][2] = uu & 0x00F000F0u;
+                  a[n][3] = vv & 0x00F000F0u;
+                }
+                const uint32_t h0 = half ? h[w].z : h[w].x, h1 = half ? h[w].w : h[w].y;
+                const uint32_t l0 = half ? l[w].z : l[w].x, l1 = half ? l[w].w : l[w].y;
+#pragma unroll
+                for (int n = 0; n < kMany; ++n) {
+                  if (w == 0 && half == 0) mma_codes_first(acc[n], a[n], h0, h1);
+                  else mma_codes(acc[n], a[n], h0, h1);
+                }
+#pragma unroll
+                for (int n = 0; n < kMany; ++n) mma_codes(acc[n], a[n], l0, l1);
+              }
+            }
+#pragma unroll
+            for (int n = 0; n < kMany; ++n)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const uint32_t w = e < 2 ? pa[n] : pb[n];
+                float& z = x[pair + n][e];
+                z = fmaf(bf16_lo(w), acc[n][e], fmaf(bf16_hi(w), (e & 1) ? qs1 : qs0, z));
+              }
+          }
+        }
+      };
+      const int first = j1 < prev0 ? 2 : (j1 < own0 ? 1 : 0);  // piece of the last key
+      const int last = j0 < prev0 ? 2 : (j0 < own0 ? 1 : 0);   // and of the first one
+      const bool whole = j1 - j0 == kTileKeys - 1;
+      if (first == last && whole) {
+        scores(std::false_type(), first, 0, kTileKeys);
+      } else {
+        int p1 = kTileKeys;
 #pragma unroll 1
-      for (int p = dlo; p <= dhi; ++p) {
-        if (p != cur) {
-          cur = p;
-#pragma unroll
-          for (int gr = 0; gr < kGr; ++gr) {
-            const uint32_t a = smem_u32(qf) +
-                               ((((p * 2) * kGr + gr) * kHeads + g) * 8 + 2 * t4) * 16;
-#pragma unroll
-            for (int w = 0; w < 2; ++w) {
-              lds128(qh[gr][w], a + w * 16);
-              lds128(ql[gr][w], a + kGr * kHeads * 128 + w * 16);
-            }
-            qs[gr][0] = qsum[(p * kHeads + 2 * t4) * kGr + gr];
-            qs[gr][1] = qsum[(p * kHeads + 2 * t4 + 1) * kGr + gr];
-          }
+        for (int p = first; p <= last; ++p) {
+          const int p0 = p == last ? 0 : (p == 0 ? own0 : prev0) - j0;
+          scores(std::true_type(), p, p0, p1);
+          p1 = p0;
         }
-#pragma unroll
-        for (int sub = 0; sub < 4; ++sub) {
-          const int r0 = sub * 16 + kr;
-          uint32_t wa[4], wb[4];
-          const uint32_t ka = tile + TL::k_word(0, 0, 0) + r0 * (D / 2) + t4 * (D / 8);
-          if (D == 128) {
-            lds128(wa, ka);
-            lds128(wb, ka + 2 * (D / 2));
-          } else {
-            lds64(wa[0], wa[1], ka);
-            lds64(wb[0], wb[1], ka + 2 * (D / 2));
-          }
-          float acc[kGr][4];
-#pragma unroll
-          for (int gr = 0; gr < kGr; ++gr) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[gr][e] = 0.f;
-#pragma unroll
-            for (int w = 0; w < 2; ++w) {
-              uint32_t u = wa[gr * 2 + w], v = wb[gr * 2 + w];
-              const uint32_t a0[4] = {u & 0x000F000Fu, v & 0x000F000Fu, u & 0x00F000F0u,
-                                      v & 0x00F000F0u};
-              u >>= 8;
-              v >>= 8;
-              const uint32_t a1[4] = {u & 0x000F000Fu, v & 0x000F000Fu, u & 0x00F000F0u,
-                                      v & 0x00F000F0u};
-              const uint32_t h0[2] = {qh[gr][w][0], qh[gr][w][1]};
-              const uint32_t h1[2] = {qh[gr][w][2], qh[gr][w][3]};
-              const uint32_t l0[2] = {ql[gr][w][0], ql[gr][w][1]};
-              const uint32_t l1[2] = {ql[gr][w][2], ql[gr][w][3]};
-              mma_f16_16816(acc[gr], a0, h0);
-              mma_f16_16816(acc[gr], a0, l0);
-              mma_f16_16816(acc[gr], a1, h1);
-              mma_f16_16816(acc[gr], a1, l1);
-            }
-          }
-          uint32_t pa[2], pb[2];
-          if (D == 128) {
-            lds64(pa[0], pa[1], tile + TL::k_param(0, 0) + r0 * 8);
-            lds64(pb[0], pb[1], tile + TL::k_param(0, 0) + r0 * 8 + 16);
-          } else {
-            pa[0] = lds32(tile + TL::k_param(0, 0) + r0 * 4);
-            pb[0] = lds32(tile + TL::k_param(0, 0) + r0 * 4 + 8);
-          }
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float main = 0.f, rest = 0.f;
-#pragma unroll
-            for (int gr = 0; gr < kGr; ++gr) {
-              const uint32_t w = e < 2 ? pa[gr] : pb[gr];
-              main = fmaf(bf16_lo(w), acc[gr][e], main);
-              rest = fmaf(bf16_hi(w), qs[gr][e & 1], rest);
-            }
-            const float y = fmaf(main, F[e & 1], rest);
-            if (dlo == dhi) {
-              x[sub][e] = y;
-            } else {  // keep the keys of piece p
-              const int j = j0 + r0 + (e & 2);
-              if (min(ci - j / s, 2) == p || p == dlo) x[sub][e] = y;
-            }
-          }
-        }
-      }
-      if (j1 - j0 != kTileKeys - 1) {  // the sequence's last tile
 #pragma unroll
         for (int sub = 0; sub < 4; ++sub)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             if (j0 + sub * 16 + kr + (e & 2) > j1) x[sub][e] = -INFINITY;
       }
+      next_part();
       float mx[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        mx[e] = fmaxf(fmaxf(fmaxf(x[0][e], x[0][e + 2]), fmaxf(x[1][e], x[1][e + 2])),
-                      fmaxf(fmaxf(x[2][e], x[2][e + 2]), fmaxf(x[3][e], x[3][e + 2])));
+        mx[e] = fmax3(fmax3(x[0][e], x[0][e + 2], x[1][e]),
+                      fmax3(x[1][e + 2], x[2][e], x[2][e + 2]), fmaxf(x[3][e], x[3][e + 2]));
 #pragma unroll
         for (int sh = 4; sh <= 16; sh <<= 1)
           mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xFFFFFFFFu, mx[e], sh));
+        mx[e] *= F[e];
       }
       if (__any_sync(0xFFFFFFFFu, mx[0] > m_run[0] || mx[1] > m_run[1])) {
 #pragma unroll
@@ -388,61 +497,72 @@ __global__ void __launch_bounds__(kDecodeThreads, 3) decode_kernel(
       }
       const float mu[2] = {m_run[0] == -INFINITY ? 0.f : m_run[0],
                            m_run[1] == -INFINITY ? 0.f : m_run[1]};
-      const bool whole = j1 - j0 == kTileKeys - 1;
 #pragma unroll
-      for (int sub = 0; sub < 4; ++sub) {
-        const int r0 = sub * 16 + kr;
-        float pr[4];
+      for (int sub = 0; sub < 4; ++sub)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          pr[e] = fast_exp2(x[sub][e] - mu[e & 1]);
-          l_run[e & 1] += pr[e];
+          x[sub][e] = fast_exp2(fmaf(x[sub][e], F[e & 1], -mu[e & 1]));
+          l_run[e & 1] += x[sub][e];
         }
-        uint32_t pa[2], pb[2];
-        if (D == 128) {
-          lds64(pa[0], pa[1], tile + TL::v_param(0, 0) + r0 * 8);
-          lds64(pb[0], pb[1], tile + TL::v_param(0, 0) + r0 * 8 + 16);
-        } else {
-          pa[0] = lds32(tile + TL::v_param(0, 0) + r0 * 4);
-          pb[0] = lds32(tile + TL::v_param(0, 0) + r0 * 4 + 8);
-        }
-        if (!whole) {  // rows past the sequence hold anything, NaN too
+      if (!warp_wait(full0 + 8 * buf, phase, abort_flag, 403)) break;
+      const uint8_t* tile = ring + buf * SM::kHalf - SM::kHalf;  // V offsets count from the tile
+      if (!whole) {  // rows past the sequence hold anything, NaN too
+        for (int r = j1 - j0 + 1 + lane; r < kTileKeys; r += 32)
 #pragma unroll
-          for (int gr = 0; gr < kGr; ++gr) {
-            if (j0 + r0 > j1) pa[gr] = 0u;
-            if (j0 + r0 + 2 > j1) pb[gr] = 0u;
+          for (int gr = 0; gr < kGr; ++gr)
+            *reinterpret_cast<uint32_t*>(const_cast<uint8_t*>(tile) + TL::v_param(r, gr)) = 0u;
+        __syncwarp();
+      }
+#pragma unroll
+      for (int gr = 0; gr < kGr; ++gr) {
+        uint32_t par[4][2], most = 0;
+        const uint8_t* vp = tile + TL::v_param(0, gr) + kr * (kGr * 4);
+#pragma unroll
+        for (int sub = 0; sub < 4; ++sub)
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            par[sub][u] = *reinterpret_cast<const uint32_t*>(vp + (sub * 16 + 2 * u) * (kGr * 4));
+            most = max_bf16x2(most, par[sub][u]);
           }
-        }
+        // scale * 2^(14 - exponent of the tile's largest scale) < 2^15, by adding
+        // to the exponent (a scale of 0 becomes some number, which its codes of 0
+        // cancel; the offset of a NaN group is NaN as well)
+        const uint32_t ex =
+            max(__reduce_max_sync(0xFFFFFFFFu, most & 0xFFFFu) >> 7, 40u);
+        const uint32_t up = (141u - ex) << 23;
+        const float down = __uint_as_float((ex - 14u) << 23);
+        float acc[4][4];
 #pragma unroll
-        for (int gr = 0; gr < kGr; ++gr) {
-          const float sa = bf16_lo(pa[gr]), sb = bf16_lo(pb[gr]);
-          const float ca = fmaf(8.f, sa, bf16_hi(pa[gr])), cb = fmaf(8.f, sb, bf16_hi(pb[gr]));
+        for (int sub = 0; sub < 4; ++sub) {
+          const float sa = __uint_as_float(par[sub][0] * 65536u + up);
+          const float sb = __uint_as_float(par[sub][1] * 65536u + up);
+          const float ca = bf16_hi(par[sub][0]), cb = bf16_hi(par[sub][1]);
+          const float* pr = x[sub];
 #pragma unroll
           for (int e = 0; e < 2; ++e)
             off[gr][e] = fmaf(pr[e], ca, fmaf(pr[e + 2], cb, off[gr][e]));
-          const uint32_t bw[2] = {movmatrix_t(pack_bf16(pr[0] * sa, pr[1] * sa)),
-                                  movmatrix_t(pack_bf16(pr[2] * sb, pr[3] * sb))};
+          const uint32_t b0 = transpose8x8(pack_half(pr[0] * sa, pr[1] * sa));
+          const uint32_t b1 = transpose8x8(pack_half(pr[2] * sb, pr[3] * sb));
           // word g of the group for keys 4 t4 .. 4 t4 + 3: MMA k rows
           // 2 t4, 2 t4 + 1 and 2 t4 + 8, 2 t4 + 9
-          uint32_t v[4];
-          lds128(v, tile + TL::v_word(0, 0, 0) + (((sub * kGr + gr) * 8 + g) * 16 + 4 * t4) * 4);
+          const uint4 v = *reinterpret_cast<const uint4*>(
+              tile + TL::v_word(0, 0, 0) + (((sub * kGr + gr) * 8 + g) * 16 + 4 * t4) * 4);
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            uint32_t ra = __byte_perm(v[0], v[1], half ? 0x7632 : 0x5410);
-            uint32_t rb = __byte_perm(v[2], v[3], half ? 0x7632 : 0x5410);
-#pragma unroll
-            for (int m = 0; m < 2; ++m) {
-              const uint32_t a[4] = {centred(ra), centred(ra >> 4), centred(rb),
-                                     centred(rb >> 4)};
-              mma_bf16_16816(o[gr * 4 + half * 2 + m], a, bw);
-              ra >>= 8;
-              rb >>= 8;
-            }
+          for (int m = 0; m < 4; ++m) {  // dims 2m (rows g) and 2m + 1 (rows g + 8)
+            const uint32_t sel = m | ((4 + m) << 8);  // byte m of either word, 16 bits apart
+            const uint32_t ra = __byte_perm(v.x, v.y, sel), rb = __byte_perm(v.z, v.w, sel);
+            const uint32_t a[4] = {ra & 0x000F000Fu, ra & 0x00F000F0u, rb & 0x000F000Fu,
+                                   rb & 0x00F000F0u};
+            if (sub == 0) mma_codes_first(acc[m], a, b0, b1);
+            else mma_codes(acc[m], a, b0, b1);
           }
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[gr * 4 + i][e] = fmaf(acc[i][e], down, o[gr * 4 + i][e]);
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(empty0 + 8 * st);
+      next_part();
     }
 #pragma unroll
     for (int sh = 4; sh <= 16; sh <<= 1) {
@@ -455,20 +575,18 @@ __global__ void __launch_bounds__(kDecodeThreads, 3) decode_kernel(
       }
     }
   }
-  __syncthreads();  // every stage is consumed: the ring holds the merge now
+  __syncthreads();  // every part is read: the rings hold the merge now
   if (*abort_flag) {  // a wait gave up: let the copies in flight land, within limits
-    if (tid == 0) {
-      const int n = *issued;
-      for (int it = max(0, n - kStages); it < n; ++it)
-        mbar_wait(full0 + 8 * (it % kStages), (it / kStages) & 1, nullptr, 403, kWaitDeadlineNs / 8);
-    }
+    if (lane == 0)
+      for (int i = 0; i < kRing; ++i)
+        mbar_wait(full0 + 8 * i, i < buf ? phase ^ 1 : phase, nullptr, 404, kWaitDeadlineNs / 8);
     return;
   }
 
   float* mo = reinterpret_cast<float*>(smem);   // [warp][head][D]
   float* mm = mo + kWarps * kHeads * D;         // [warp][head]
   float* ml = mm + kWarps * kHeads;             // [warp][head]
-  if (warp < kWarps) {
+  {
 #pragma unroll
     for (int gr = 0; gr < kGr; ++gr)
 #pragma unroll
@@ -477,8 +595,8 @@ __global__ void __launch_bounds__(kDecodeThreads, 3) decode_kernel(
         for (int e = 0; e < 2; ++e) {
           // rows g and g + 8 are dims 2m and 2m + 1 of word g
           float* at = mo + (warp * kHeads + 2 * t4 + e) * D + gr * 64 + 8 * g + 2 * m;
-          at[0] = o[gr * 4 + m][e] + off[gr][e];
-          at[1] = o[gr * 4 + m][e + 2] + off[gr][e];
+          at[0] = fmaf(o[gr * 4 + m][e], 16777216.f, off[gr][e]);     // 2^24
+          at[1] = fmaf(o[gr * 4 + m][e + 2], 1048576.f, off[gr][e]);  // 2^24 / 16
         }
     if (g == 0) {
 #pragma unroll
@@ -503,27 +621,28 @@ __global__ void __launch_bounds__(kDecodeThreads, 3) decode_kernel(
       acc += f * mo[(w * kHeads + hh) * D + d];
       lsum += f * ml[w * kHeads + hh];
     }
-    const size_t slot = ((size_t)b * Hq + h_base + hh) * shares + sp;
+    const size_t slot = ((size_t)seq * per_seq + unit + blockIdx.x) * kHeads + hh;
     Opart[slot * D + d] = acc;
-    if (d == 0) {
-      MLpart[slot * 2] = M;
-      MLpart[slot * 2 + 1] = lsum;
-    }
+    if (d == 0) MLpart[slot] = make_float2(M, lsum);
+  }
+  // the buffers go back to the copies of the next piece
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
 }
 
-// O = sum_p e^{m_p - m} O_p / sum_p e^{m_p - m} l_p over the shares that hold
-// keys, LSE = m + ln(sum): one block a (head, sequence), four rows of D/4
-// threads over the shares in turn.
+// O = sum_p e^{m_p - m} O_p / sum_p e^{m_p - m} l_p over the partial results of
+// a unit, LSE = m + ln(sum): one block a (head, sequence), four rows of D/4
+// threads over the partials in turn.
 template <int D>
 __global__ void __launch_bounds__(D) decode_merge(const float* __restrict__ Opart,
-                                                  const float* __restrict__ MLpart,
+                                                  const float2* __restrict__ MLpart,
                                                   const int* __restrict__ t,
                                                   __nv_bfloat16* __restrict__ O,
-                                                  float* __restrict__ LSE, int Hq, int cap,
-                                                  int shares) {
+                                                  float* __restrict__ LSE, int B, int Hq, int Hkv,
+                                                  int n_hg, long long cap, int grid_shares) {
   __shared__ float4 part[4][D / 4];
   __shared__ float stat[2];
+  __shared__ long long sums[D / 32];
   const int h = blockIdx.x, b = blockIdx.y, d = threadIdx.x;
   const int tb = __ldg(t + b);
   const size_t row = (size_t)b * Hq + h;
@@ -532,17 +651,27 @@ __global__ void __launch_bounds__(D) decode_merge(const float* __restrict__ Opar
     if (d == 0) LSE[row] = __int_as_float(0x7fc00000);
     return;
   }
-  const int tiles = tb / kTileKeys + 1, per = tiles_per_share(tiles, shares);
-  const int n = (tiles + per - 1) / per;
-  const float2* ml = reinterpret_cast<const float2*>(MLpart) + row * shares;
+  const int G = Hq / Hkv, per_seq = Hkv * n_hg;
+  const int unit = h / G * n_hg + h % G / kHeads, hh = h % G % kHeads;
+  const Split split = make_split(spans_before(t, B, cap, sums) * per_seq, grid_shares);
+  const int tiles = tiles_of(tb, cap);
+  const long long g0 =
+      spans_before(t, b, cap, sums) * per_seq + (long long)unit * (tiles + kSetup) + kSetup;
+  const long long c0 = share_of(split, g0);
+  const int n = (int)(share_of(split, g0 + tiles - 1) - c0) + 1;
+  const size_t slot0 = ((size_t)b * per_seq + unit + c0) * kHeads + hh;
+  const float2* ml = MLpart + slot0;
   if (d < 32) {
     float M = -INFINITY;
-    for (int p = d; p < n; p += 32) M = fmaxf(M, ml[p].x);
+    for (int p = d; p < n; p += 32) M = fmaxf(M, ml[(size_t)p * kHeads].x);
 #pragma unroll
     for (int sh = 16; sh >= 1; sh >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, sh));
     const float mu = M == -INFINITY ? 0.f : M;
     float l = 0.f;
-    for (int p = d; p < n; p += 32) l += fast_exp2(ml[p].x - mu) * ml[p].y;
+    for (int p = d; p < n; p += 32) {
+      const float2 v = ml[(size_t)p * kHeads];
+      l += fast_exp2(v.x - mu) * v.y;
+    }
 #pragma unroll
     for (int sh = 16; sh >= 1; sh >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, sh);
     if (d == 0) {
@@ -553,12 +682,12 @@ __global__ void __launch_bounds__(D) decode_merge(const float* __restrict__ Opar
   __syncthreads();
   const float M = stat[0], l = stat[1];
   const int lane = d % (D / 4), first = d / (D / 4);
-  const float4* src = reinterpret_cast<const float4*>(Opart) + row * shares * (D / 4) + lane;
+  const float4* src = reinterpret_cast<const float4*>(Opart) + slot0 * (D / 4) + lane;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
   for (int p = first; p < n; p += 4) {
-    const float f = fast_exp2(ml[p].x - M);
-    const float4 v = src[(size_t)p * (D / 4)];
+    const float f = fast_exp2(ml[(size_t)p * kHeads].x - M);
+    const float4 v = src[(size_t)p * kHeads * (D / 4)];
     acc.x = fmaf(f, v.x, acc.x);
     acc.y = fmaf(f, v.y, acc.y);
     acc.z = fmaf(f, v.z, acc.z);
@@ -576,30 +705,33 @@ template <int D>
 cudaError_t launch_decode_t(const void* q, const Pages& pg, const int* t, void* O, float* LSE,
                             int B, int Hq, int s, int c, float base, float scale,
                             void* workspace, cudaStream_t stream) {
-  const int cap = pg.max_blocks * pg.block_rows;
-  const int shares = decode_shares(B, Hq, pg.Hkv, cap);
-  const int n_hg = (Hq / pg.Hkv + kHeads - 1) / kHeads;
+  const long long cap = (long long)pg.max_blocks * pg.block_rows;
+  const int shares = (int)decode_shares(B, Hq, pg.Hkv, cap);
+  const int n_hg = head_groups(Hq, pg.Hkv);
+  const size_t slots = ((size_t)B * pg.Hkv * n_hg + shares) * kHeads;
   float* Opart = static_cast<float*>(workspace);
-  float* MLpart = Opart + (size_t)B * Hq * shares * D;
+  float2* MLpart = reinterpret_cast<float2*>(Opart + slots * D);
   auto kern = decode_kernel<D>;
   constexpr int smem = DecodeSmem<D>::kTotal;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  kern<<<dim3(shares, pg.Hkv * n_hg, B), kDecodeThreads, smem, stream>>>(
-      static_cast<const __nv_bfloat16*>(q), pg, t, Opart, MLpart, Hq, s, c,
-      scale * 1.4426950408889634f, shares, n_hg, make_theta(D, base));
+  kern<<<shares, kDecodeThreads, smem, stream>>>(
+      static_cast<const __nv_bfloat16*>(q), pg, t, Opart, MLpart, B, Hq, s, c,
+      scale * 1.4426950408889634f, n_hg, make_theta(D, base));
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   decode_merge<D><<<dim3(Hq, B), D, 0, stream>>>(Opart, MLpart, t,
-                                                 static_cast<__nv_bfloat16*>(O), LSE, Hq, cap,
-                                                 shares);
+                                                 static_cast<__nv_bfloat16*>(O), LSE, B, Hq,
+                                                 pg.Hkv, n_hg, cap, shares);
   return cudaGetLastError();
 }
 
 }  // namespace kv4
 
 size_t kv4_decode_workspace_bytes(int B, int Hq, int Hkv, int D, long long cap) {
-  return (size_t)B * Hq * kv4::decode_shares(B, Hq, Hkv, cap) * (D + 2) * sizeof(float);
+  const size_t units = (size_t)B * Hkv * kv4::head_groups(Hq, Hkv);
+  const size_t slots = units + (size_t)kv4::decode_shares(B, Hq, Hkv, cap);
+  return B == 0 ? 0 : slots * kv4::kHeads * (D + 2) * sizeof(float);
 }
 
 cudaError_t launch_kv4_decode(const void* q, const void* pool, const int* block_table,

@@ -71,6 +71,36 @@ inline Theta make_theta(int D, float base) {
   return t;
 }
 
+// cos and sin of a double angle (any size up to about 2^31 radians): reduced to
+// |r| <= pi/4 by the nearest multiple of pi/2 (in two parts), then the Taylor
+// series to r^16 (truncation below 1e-15).
+__device__ __forceinline__ void sincos64(double a, double& c, double& s) {
+  const double n = rint(a * 0.63661977236758134308);
+  double r = fma(-n, 1.57079632679489655800, a);
+  r = fma(-n, 6.12323399573676603587e-17, r);
+  const double z = r * r;
+  double p = fma(z, 1.0 / 355687428096000.0, -1.0 / 1307674368000.0);
+  p = fma(z, p, 1.0 / 6227020800.0);
+  p = fma(z, p, -1.0 / 39916800.0);
+  p = fma(z, p, 1.0 / 362880.0);
+  p = fma(z, p, -1.0 / 5040.0);
+  p = fma(z, p, 1.0 / 120.0);
+  p = fma(z, p, -1.0 / 6.0);
+  const double sr = fma(r * z, p, r);
+  double q = fma(z, 1.0 / 20922789888000.0, -1.0 / 87178291200.0);
+  q = fma(z, q, 1.0 / 479001600.0);
+  q = fma(z, q, -1.0 / 3628800.0);
+  q = fma(z, q, 1.0 / 40320.0);
+  q = fma(z, q, -1.0 / 720.0);
+  q = fma(z, q, 1.0 / 24.0);
+  q = fma(z, q, -0.5);
+  const double cr = fma(z, q, 1.0);
+  const int k = (int)((long long)n & 3);
+  const double u = (k & 1) ? sr : cr, v = (k & 1) ? cr : sr;
+  c = (k == 1 || k == 2) ? -u : u;
+  s = (k >= 2) ? -v : v;
+}
+
 // Where a paged cache lives: pool of num_blocks pages, block_table [B][max_blocks].
 struct Pages {
   uint8_t* pool;

@@ -185,10 +185,10 @@ def test_tile_and_workspace_sizes(lib):
     assert dca.dca_kv4_tile_bytes(96) == 0
     assert dca.dca_attn_decode_kv4_workspace(0, 8, 1, 128, 64) == 0
     one = dca.dca_attn_decode_kv4_workspace(1, 8, 1, 128, 64)
-    assert one == 8 * 130 * 4  # one tile: one share
+    assert one == 2 * 8 * 130 * 4  # one unit of one tile: a slot for either, 8 heads each
     assert dca.dca_attn_decode_kv4_workspace(1, 8, 3, 128, 64) == 0
     assert dca.dca_attn_decode_kv4_workspace(1, 8, 1, 128, 0) == 0
-    assert dca.dca_attn_decode_kv4_workspace(16, 64, 8, 128, 65536) % (16 * 64 * 130 * 4) == 0
+    assert dca.dca_attn_decode_kv4_workspace(1, 8, 1, 64, 128) == 3 * 8 * 66 * 4
     assert dca.dca_pages_workspace(0, 1, 1) > 0 and dca.dca_pages_workspace(-1, 1, 1) == 0
     assert dca.dca_pages_workspace(4, 0, 10) == 0 and dca.dca_pages_workspace(4, 3, 0) == 0
 
