@@ -12,7 +12,6 @@ Build the library with ``python -m long_context_attention_dca_b200.build``.
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 
@@ -554,16 +553,28 @@ def dca_kv_append_paged(k_new, v_new, Kpool, Vpool, block_table, t, s, c, base=1
                                      _stream(k_new)))
 
 
-def _on_device(first: torch.Tensor, *others):
-    """The context that makes `first`'s device current for the launches; the
-    other tensors (or None) must be on it too."""
-    dev = first.device
-    for t in others:
-        if t is not None and t.device != dev:
+# The handle of a device's current stream; the torch.cuda call costs microseconds
+# more than the launch it serves.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _call(name: str, dev: torch.device, *args) -> None:
+    """Call the entry point `name` with its stream argument, `dev` current."""
+    fn, index = getattr(_lib or lib(), name), dev.index
+    if index == torch.cuda.current_device():
+        status = fn(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, _raw_stream(index))
+    if status:
+        _check(status)
+
+
+def _same_device(dev: torch.device, *tensors) -> None:
+    for t in tensors:
+        if t.device != dev:
             raise DcaError(1, f"tensors on {dev} and {t.device}")
-    if dev.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(dev)
 
 
 def dca_kv4_tile_bytes(D: int) -> int:
@@ -581,15 +592,15 @@ def _kv4_pool(pool, D):
 
 
 def _kv4_rows(cu_seqlens, t0, block_table):
-    """B of a packed call over a block table."""
+    """(B, max_blocks) of a packed call over a block table."""
     _need(block_table, "block_table", torch.int32, 2)
     _need(cu_seqlens, "cu_seqlens", torch.int32, 1)
     _need(t0, "t0", torch.int32, 1)
-    B = block_table.shape[0]
+    B, max_blocks = block_table.shape
     if cu_seqlens.numel() != B + 1 or t0.numel() != B:
         raise DcaError(1, f"cu_seqlens and t0 must have {B + 1} and {B} entries, got "
                           f"{cu_seqlens.numel()} and {t0.numel()}")
-    return B
+    return B, max_blocks
 
 
 def dca_kv4_append_paged(k_new, v_new, pool, block_table, cu_seqlens, t0, s, c, base=10000.0):
@@ -603,12 +614,12 @@ def dca_kv4_append_paged(k_new, v_new, pool, block_table, cu_seqlens, t0, s, c, 
     num_blocks, pool_heads, block_rows = _kv4_pool(pool, D)
     if v_new.shape != k_new.shape or pool_heads != Hkv:
         raise DcaError(1, "k_new, v_new and pool disagree on rows or heads")
-    B = _kv4_rows(cu_seqlens, t0, block_table)
-    with _on_device(k_new, v_new, pool, block_table, cu_seqlens, t0):
-        _check(lib().dca_kv4_append_paged(
-            _ptr(k_new), _ptr(v_new), _ptr(pool), _ptr(block_table), block_table.shape[1],
-            block_rows, num_blocks, _ptr(cu_seqlens), _ptr(t0), B, T, Hkv, D, s, c, base,
-            _stream(k_new)))
+    B, max_blocks = _kv4_rows(cu_seqlens, t0, block_table)
+    dev = k_new.device
+    _same_device(dev, v_new, pool, block_table, cu_seqlens, t0)
+    _call("dca_kv4_append_paged", dev, k_new.data_ptr(), v_new.data_ptr(), pool.data_ptr(),
+          block_table.data_ptr(), max_blocks, block_rows, num_blocks, cu_seqlens.data_ptr(),
+          t0.data_ptr(), B, T, Hkv, D, s, c, base)
 
 
 def dca_kv4_read_paged(pool, block_table, cu_seqlens, t0, T, D, K=None, V=None):
@@ -616,22 +627,27 @@ def dca_kv4_read_paged(pool, block_table, cu_seqlens, t0, T, D, K=None, V=None):
     positions t0[b], t0[b]+1, .. at rows cu_seqlens[b] .. cu_seqlens[b+1]-1.
     With K, V [B, rows, Hkv, D] given, position p goes to row p of entry b."""
     num_blocks, Hkv, block_rows = _kv4_pool(pool, D)
-    B = _kv4_rows(cu_seqlens, t0, block_table)
+    B, max_blocks = _kv4_rows(cu_seqlens, t0, block_table)
     if (K is None) != (V is None):
         raise DcaError(1, "K and V are given together or not at all")
+    dev, out_rows = pool.device, 0
     if K is None:
-        K = torch.empty((T, Hkv, D), dtype=torch.bfloat16, device=pool.device)
+        K = torch.empty((T, Hkv, D), dtype=torch.bfloat16, device=dev)
         V = torch.empty_like(K)
-    _need(K, "K", torch.bfloat16, K.dim())
-    _need(V, "V", torch.bfloat16, K.dim())
-    shape = (T, Hkv, D) if K.dim() == 3 else (B, K.shape[1], Hkv, D)
-    if tuple(K.shape) != shape or tuple(V.shape) != shape:
-        raise DcaError(1, f"K and V must be {shape}, got {tuple(K.shape)} and {tuple(V.shape)}")
-    with _on_device(pool, block_table, cu_seqlens, t0, K, V):
-        _check(lib().dca_kv4_read_paged(
-            _ptr(pool), _ptr(block_table), block_table.shape[1], block_rows, num_blocks,
-            _ptr(cu_seqlens), _ptr(t0), _ptr(K), _ptr(V), B, T, Hkv, D,
-            0 if K.dim() == 3 else K.shape[1], _stream(pool)))
+    else:
+        packed = isinstance(K, torch.Tensor) and K.dim() == 3
+        _need(K, "K", torch.bfloat16, 3 if packed else 4)
+        _need(V, "V", torch.bfloat16, 3 if packed else 4)
+        out_rows = 0 if packed else K.shape[1]
+        shape = (T, Hkv, D) if packed else (B, out_rows, Hkv, D)
+        if tuple(K.shape) != shape or tuple(V.shape) != shape or (not packed and out_rows == 0):
+            raise DcaError(1, f"K and V must be {shape}, got {tuple(K.shape)} and "
+                              f"{tuple(V.shape)}")
+        _same_device(dev, K, V)
+    _same_device(dev, block_table, cu_seqlens, t0)
+    _call("dca_kv4_read_paged", dev, pool.data_ptr(), block_table.data_ptr(), max_blocks,
+          block_rows, num_blocks, cu_seqlens.data_ptr(), t0.data_ptr(), K.data_ptr(),
+          V.data_ptr(), B, T, Hkv, D, out_rows)
     return K, V
 
 
@@ -652,20 +668,27 @@ def dca_attn_decode_kv4_paged(q, pool, block_table, t, s, c, base=10000.0, scale
     max_blocks = block_table.shape[1]
     if block_table.shape[0] != B or t.numel() != B:
         raise DcaError(1, f"block_table and t must have {B} rows")
-    O = torch.empty_like(q) if O is None else O
-    LSE = torch.empty((B, Hq), dtype=torch.float32, device=q.device) if LSE is None else LSE
-    _need(O, "O", torch.bfloat16, 3)
-    _need(LSE, "LSE", torch.float32, 2)
-    if O.shape != q.shape or tuple(LSE.shape) != (B, Hq):
-        raise DcaError(1, "O must have the shape of q and LSE [B, Hq]")
+    dev = q.device
+    if O is None:
+        O = torch.empty_like(q)
+    else:
+        _need(O, "O", torch.bfloat16, 3)
+        if O.shape != q.shape:
+            raise DcaError(1, "O must have the shape of q")
+    if LSE is None:
+        LSE = torch.empty((B, Hq), dtype=torch.float32, device=dev)
+    else:
+        _need(LSE, "LSE", torch.float32, 2)
+        if tuple(LSE.shape) != (B, Hq):
+            raise DcaError(1, f"LSE must be {(B, Hq)}, got {tuple(LSE.shape)}")
     if workspace is None:
         workspace = _workspace(dca_attn_decode_kv4_workspace(B, Hq, Hkv, D,
-                                                             max_blocks * block_rows), q.device)
-    with _on_device(q, pool, block_table, t, O, LSE, workspace):
-        _check(lib().dca_attn_decode_kv4_paged(
-            _ptr(q), _ptr(pool), _ptr(block_table), max_blocks, block_rows, num_blocks, _ptr(t),
-            _ptr(O), _ptr(LSE), B, Hq, Hkv, D, s, c, base, scale, _ptr(workspace),
-            workspace.numel(), _stream(q)))
+                                                             max_blocks * block_rows), dev)
+    _same_device(dev, pool, block_table, t, O, LSE, workspace)
+    _call("dca_attn_decode_kv4_paged", dev, q.data_ptr(), pool.data_ptr(),
+          block_table.data_ptr(), max_blocks, block_rows, num_blocks, t.data_ptr(), O.data_ptr(),
+          LSE.data_ptr(), B, Hq, Hkv, D, s, c, base, scale, workspace.data_ptr(),
+          workspace.nbytes)
     return O, LSE
 
 
@@ -673,59 +696,63 @@ class _PagePool(ctypes.Structure):
     _fields_ = [("base", _P), ("unit_bytes", _Z), ("outer", _I), ("unit_rows", _I)]
 
 
-def _page_pools(pools, num_blocks, block_rows, device):
+def _page_pools(pools, num_blocks, block_rows, dev):
     """The descriptors of pools with pages of block_rows rows: bf16 [num_blocks,
     block_rows, Hkv, D], 4-bit uint8 [num_blocks, Hkv, block_rows / 64, tile],
     given one by one or stacked in one 5-d tensor."""
-    if isinstance(pools, torch.Tensor):
-        stacked = pools.dim() == 5
-        given = [(pools, pools.shape[0] if stacked else 1, 1 if stacked else 0)]
-    else:
-        given = [(p, 1, 0) for p in pools]
-    out = (_PagePool * max(1, sum(n for _, n, _ in given)))()
-    at = 0
-    for p, n, lead in given:
-        if not isinstance(p, torch.Tensor) or not p.is_cuda or p.device != device:
-            raise DcaError(1, f"pools must be tensors on {device}")
-        if p.dim() != 4 + lead or not p.is_contiguous() or p.shape[lead] != num_blocks:
+    found = []
+    for p in [pools] if isinstance(pools, torch.Tensor) else pools:
+        if not isinstance(p, torch.Tensor) or p.device != dev:
+            raise DcaError(1, f"pools must be tensors on {dev}")
+        shape = p.shape
+        lead = 1 if p is pools and len(shape) == 5 else 0
+        if len(shape) != 4 + lead or not p.is_contiguous() or shape[lead] != num_blocks:
             raise DcaError(1, f"a pool must be contiguous with {num_blocks} pages, got "
-                              f"{tuple(p.shape)}")
-        a, b, width = p.shape[lead + 1:]
+                              f"{tuple(shape)}")
+        a, b, width = shape[lead + 1:]
         if p.dtype == torch.uint8 and b * 64 == block_rows:
-            desc = (width, a, 64)
+            desc, page = (width, a, 64), a * b * width
         elif p.dtype == torch.bfloat16 and a == block_rows:
-            desc = (2 * b * width, 1, 1)
+            desc, page = (2 * b * width, 1, 1), 2 * a * b * width
         else:
-            raise DcaError(1, f"a pool of {p.dtype} {tuple(p.shape)} has no pages of "
+            raise DcaError(1, f"a pool of {p.dtype} {tuple(shape)} has no pages of "
                               f"{block_rows} rows")
-        base, step = p.data_ptr(), p.stride(0) * p.element_size()
-        for i in range(n):
-            out[at] = (base + i * step, *desc)
-            at += 1
-    return out, at
+        base = p.data_ptr()
+        for i in range(shape[0] if lead else 1):
+            found.append((base + i * page * num_blocks, *desc))
+    return (_PagePool * max(1, len(found)))(*found), len(found)
 
 
-def _page_state(block_table, refs, lens, outs):
-    """Check the page state and allocate the outputs that were not given."""
-    _need(block_table, "block_table", torch.int32, 2)
-    _need(refs, "refs", torch.int32, 1)
-    B = block_table.shape[0]
-    for name, x in lens:
+def _page_lists(B, *lists):
+    for name, x in lists:
         _need(x, name, torch.int32, 1)
         if x.numel() != B:
             raise DcaError(1, f"{name} must have {B} entries, got {x.numel()}")
-    got = []
-    for name, x, like in outs:
-        x = torch.empty_like(like) if x is None else x
-        _need(x, name, torch.int32, like.dim())
-        if x.shape != like.shape:
-            raise DcaError(1, f"{name} must be {tuple(like.shape)}, got {tuple(x.shape)}")
-        got.append(x)
-    return got
+
+
+def _page_out(name, x, like):
+    """An output like the tensor it replaces: as given, or new."""
+    if x is None:
+        return torch.empty_like(like)
+    _need(x, name, torch.int32, like.dim())
+    if x.shape != like.shape:
+        raise DcaError(1, f"{name} must be {tuple(like.shape)}, got {tuple(x.shape)}")
+    return x
 
 
 def dca_pages_workspace(B: int, max_blocks: int, num_blocks: int) -> int:
     return int(lib().dca_pages_workspace(B, max_blocks, num_blocks))
+
+
+def _page_scratch(refs, info, workspace, B, max_blocks):
+    if info is None:
+        info = refs.new_empty(2)
+    _need(info, "info", torch.int32, 1)
+    if info.numel() < 2:
+        raise DcaError(1, "info must have 2 entries")
+    if workspace is None:
+        workspace = refs.new_empty(-(-dca_pages_workspace(B, max_blocks, refs.numel()) // 4))
+    return info, workspace
 
 
 def dca_pages_remap(src, old_len, new_len, block_table, refs, pools, block_rows, workspace=None,
@@ -735,23 +762,20 @@ def dca_pages_remap(src, old_len, new_len, block_table, refs, pools, block_rows,
     max_blocks]; refs int32 [num_blocks]; pools: tensors whose partial pages are
     copied, one by one or stacked.  Returns (block_table, refs, info), new
     tensors unless given (a given one may be the one it replaces)."""
-    table_out, counts_out = _page_state(
-        block_table, refs, (("src", src), ("old_len", old_len), ("new_len", new_len)),
-        (("block_table_out", block_table_out, block_table), ("refs_out", refs_out, refs)))
-    if info is None:
-        info = torch.empty(2, dtype=torch.int32, device=refs.device)
-    _need(info, "info", torch.int32, 1)
+    _need(block_table, "block_table", torch.int32, 2)
+    _need(refs, "refs", torch.int32, 1)
     B, max_blocks = block_table.shape
-    num_blocks = refs.numel()
-    desc, n = _page_pools(pools, num_blocks, block_rows, refs.device)
-    if workspace is None:
-        workspace = _workspace(dca_pages_workspace(B, max_blocks, num_blocks), refs.device)
-    with _on_device(refs, src, old_len, new_len, block_table, table_out, counts_out, info,
-                    workspace):
-        _check(lib().dca_pages_remap(
-            _ptr(src), _ptr(old_len), _ptr(new_len), _ptr(block_table), _ptr(refs),
-            _ptr(table_out), _ptr(counts_out), _ptr(info), B, max_blocks, num_blocks, block_rows,
-            ctypes.byref(desc), n, _ptr(workspace), workspace.numel(), _stream(refs)))
+    num_blocks, dev = refs.numel(), refs.device
+    _page_lists(B, ("src", src), ("old_len", old_len), ("new_len", new_len))
+    table_out = _page_out("block_table_out", block_table_out, block_table)
+    counts_out = _page_out("refs_out", refs_out, refs)
+    desc, n = _page_pools(pools, num_blocks, block_rows, dev)
+    info, workspace = _page_scratch(refs, info, workspace, B, max_blocks)
+    _same_device(dev, src, old_len, new_len, block_table, table_out, counts_out, info, workspace)
+    _call("dca_pages_remap", dev, src.data_ptr(), old_len.data_ptr(), new_len.data_ptr(),
+          block_table.data_ptr(), refs.data_ptr(), table_out.data_ptr(), counts_out.data_ptr(),
+          info.data_ptr(), B, max_blocks, num_blocks, block_rows, ctypes.addressof(desc), n,
+          workspace.data_ptr(), workspace.nbytes)
     return table_out, counts_out, info
 
 
@@ -760,23 +784,21 @@ def dca_pages_compact(lens, block_table, refs, pools, block_rows, workspace=None
     """Move all pages in use to the front of their pools (see dca.h).  lens int32
     [B], the rest as dca_pages_remap.  Returns (block_table, refs, moved, info)
     with moved int32 [num_blocks], the new index of every page (-1: free)."""
-    table_out, counts_out, moved = _page_state(
-        block_table, refs, (("lens", lens),),
-        (("block_table_out", block_table_out, block_table), ("refs_out", refs_out, refs),
-         ("moved", moved, refs)))
-    if info is None:
-        info = torch.empty(2, dtype=torch.int32, device=refs.device)
-    _need(info, "info", torch.int32, 1)
+    _need(block_table, "block_table", torch.int32, 2)
+    _need(refs, "refs", torch.int32, 1)
     B, max_blocks = block_table.shape
-    num_blocks = refs.numel()
-    desc, n = _page_pools(pools, num_blocks, block_rows, refs.device)
-    if workspace is None:
-        workspace = _workspace(dca_pages_workspace(B, max_blocks, num_blocks), refs.device)
-    with _on_device(refs, lens, block_table, table_out, counts_out, moved, info, workspace):
-        _check(lib().dca_pages_compact(
-            _ptr(lens), _ptr(block_table), _ptr(refs), _ptr(table_out), _ptr(counts_out),
-            _ptr(moved), _ptr(info), B, max_blocks, num_blocks, block_rows, ctypes.byref(desc), n,
-            _ptr(workspace), workspace.numel(), _stream(refs)))
+    num_blocks, dev = refs.numel(), refs.device
+    _page_lists(B, ("lens", lens))
+    table_out = _page_out("block_table_out", block_table_out, block_table)
+    counts_out = _page_out("refs_out", refs_out, refs)
+    moved = _page_out("moved", moved, refs)
+    desc, n = _page_pools(pools, num_blocks, block_rows, dev)
+    info, workspace = _page_scratch(refs, info, workspace, B, max_blocks)
+    _same_device(dev, lens, block_table, table_out, counts_out, moved, info, workspace)
+    _call("dca_pages_compact", dev, lens.data_ptr(), block_table.data_ptr(), refs.data_ptr(),
+          table_out.data_ptr(), counts_out.data_ptr(), moved.data_ptr(), info.data_ptr(), B,
+          max_blocks, num_blocks, block_rows, ctypes.addressof(desc), n, workspace.data_ptr(),
+          workspace.nbytes)
     return table_out, counts_out, moved, info
 
 

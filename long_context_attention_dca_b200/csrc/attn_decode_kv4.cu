@@ -62,15 +62,18 @@ __device__ __forceinline__ long long share_of(const Split& sp, long long g) {
   return ((g + 1) * sp.shares - 1) / sp.tiles;
 }
 inline int head_groups(int Hq, int Hkv) { return (Hq / Hkv + kHeads - 1) / kHeads; }
-// Most shares of a call (the grid): all SMs once, or more where a share would
-// pass kMaxTiles.  The kernels use fewer when that leaves a share under one
-// tile a warp.
+// Shares of `tiles` tiles: one for every four (a tile a warp), at most `most`.
+__host__ __device__ inline long long share_count(long long tiles, long long most) {
+  const long long n = tiles / kWarps < most ? tiles / kWarps : most;
+  return n > 0 ? n : 1;
+}
+// Shares of a call whose caches are full (the grid): at most all SMs once, or
+// more where a share would pass kMaxTiles.
 inline long long decode_shares(int B, int Hq, int Hkv, long long cap) {
   const long long tiles = (long long)B * Hkv * head_groups(Hq, Hkv) *
                           ((cap + kTileKeys - 1) / kTileKeys + kSetup);
   const long long need = (tiles + kMaxTiles - 1) / kMaxTiles;
-  const long long most = need > 148 * kCtasPerSm ? need : 148 * kCtasPerSm;
-  return most < tiles ? most : (tiles > 0 ? tiles : 1);
+  return share_count(tiles, need > 148 * kCtasPerSm ? need : 148 * kCtasPerSm);
 }
 
 template <int D>
@@ -153,11 +156,6 @@ __device__ __forceinline__ long long spans_before(const int* t, int n, long long
   for (int w = 0; w < (int)(blockDim.x >> 5); ++w) x += sums[w];
   return x;
 }
-__device__ __forceinline__ Split make_split(long long tiles, long long most) {
-  long long n = tiles / kWarps;
-  n = n < most ? n : most;
-  return Split{tiles, n > 0 ? n : 1};
-}
 
 template <int D>
 __global__ void __launch_bounds__(kDecodeThreads, kCtasPerSm) decode_kernel(
@@ -182,7 +180,8 @@ __global__ void __launch_bounds__(kDecodeThreads, kCtasPerSm) decode_kernel(
   const int G = Hq / pg.Hkv, per_seq = pg.Hkv * n_hg;
   const int tpb = pg.block_rows / kTileKeys;
   const long long cap = (long long)pg.max_blocks * pg.block_rows;
-  const Split split = make_split(spans_before(t, B, cap, sums) * per_seq, gridDim.x);
+  const long long all = spans_before(t, B, cap, sums) * per_seq;
+  const Split split{all, share_count(all, gridDim.x)};
   if (blockIdx.x == 0) {  // positions outside the cache: reported, no work
     for (int b = tid; b < B; b += kDecodeThreads)
       if (tiles_of(__ldg(t + b), cap) == 0) report_error(kDevBadArg, 207);
@@ -653,7 +652,8 @@ __global__ void __launch_bounds__(D) decode_merge(const float* __restrict__ Opar
   }
   const int G = Hq / Hkv, per_seq = Hkv * n_hg;
   const int unit = h / G * n_hg + h % G / kHeads, hh = h % G % kHeads;
-  const Split split = make_split(spans_before(t, B, cap, sums) * per_seq, grid_shares);
+  const long long all = spans_before(t, B, cap, sums) * per_seq;
+  const Split split{all, share_count(all, grid_shares)};
   const int tiles = tiles_of(tb, cap);
   const long long g0 =
       spans_before(t, b, cap, sums) * per_seq + (long long)unit * (tiles + kSetup) + kSetup;

@@ -167,11 +167,13 @@ struct PoolDesc {
   int chunks, items;  // per part and per page (filled by the launcher)
 };
 constexpr int kMaxPools = 256;
-struct PoolList {
+template <int N>
+struct Pools {
   long long items;  // of one page over all pools (filled by the launcher)
   int n;
-  PoolDesc p[kMaxPools];
+  PoolDesc p[N];
 };
+using PoolList = Pools<kMaxPools>;
 size_t pages_workspace_bytes(int B, int max_blocks, int num_blocks);
 cudaError_t launch_pages_remap(const int* src, const int* old_len, const int* new_len,
                                const int* table_in, int* table_out, const int* refs_in,

@@ -17,6 +17,7 @@
 #include "dca_common.cuh"
 #include "dca_kernels.cuh"
 #include "kv4.cuh"
+#include "softmax_sm100.cuh"
 
 namespace dca {
 namespace kv4 {
@@ -64,76 +65,101 @@ __device__ __forceinline__ uint32_t min_negmax(const uint32_t (&w)[4]) {
   return as_u32(__hmin2_nan(as_bf162(lo), as_bf162(hi)));
 }
 
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
 struct Params {
-  float off, scale;  // bf16 values
-  float k1, k0;      // quotient = x * k1 + k0
-  float tol;         // how close to a border the fp32 quotient decides nothing
-  uint32_t word;     // as stored
+  float off, scale;     // halves of the bf16 values: ranges of any size stay finite
+  float inv;            // 1 / scale (of the halves)
+  uint32_t word;        // as stored
 };
+// 1 / x within a few last places (quantise8 corrects the quotient); infinite for
+// a subnormal x.
+__device__ __forceinline__ float approx_rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 // Parameters of a group from its (least, -greatest).
 __device__ __forceinline__ Params make_params(uint32_t mm) {
   Params p;
   // (-0 becomes 0, so that a stored parameter never carries a stray sign)
   const float lo = __fadd_rn(bf16_lo(mm), 0.f), hi = __fadd_rn(-bf16_hi(mm), 0.f);
-  // halves, so that the range of any two finite bf16 stays finite; rounded up
-  // twice in fp32 and then to bf16, which gives the smallest bf16 >= range / 15
-  // (15 * bf16 fits fp32, so no intermediate step can jump over it)
-  const float r = __fdiv_ru(__fsub_ru(hi * 0.5f, lo * 0.5f), 7.5f);
-  const uint32_t sb = (__float_as_uint(r) + 0xFFFFu) & 0xFFFF0000u;
-  p.off = lo;
-  p.scale = __uint_as_float(sb);
-  if (!(fabsf(lo) < INFINITY && fabsf(hi) < INFINITY)) {
-    p.word = 0x7FFF7FFFu;
-    p.k1 = p.k0 = p.tol = 0.f;
-    return p;
-  }
-  const bool plain = p.scale >= 1e-30f;
-  const float inv = plain ? 1.f / p.scale : 0.f;
-  p.k1 = inv;
-  p.k0 = -(lo * inv);
-  // |error of the quotient| <= 2^-24 (3 |k0| + 31); a scale whose reciprocal
-  // could overflow leaves every element to the exact rule
-  p.tol = plain ? fmaf(fabsf(p.k0), 4e-7f, 8e-6f) : (p.scale > 0.f ? INFINITY : 0.f);
+  // The smallest bf16 b with 15 b >= the range: from an approximate quotient cut
+  // to bf16, stepped up while 7.5 b, exact in fp32, is below half the range.
+  const float range = __fsub_ru(hi * 0.5f, lo * 0.5f);
+  uint32_t sb = __float_as_uint(range * (1.f / 7.5f)) & 0xFFFF0000u;
+  if (__uint_as_float(sb) * 7.5f < range) sb += 0x10000u;
+  if (__uint_as_float(sb) * 7.5f < range) sb += 0x10000u;
+  p.off = lo * 0.5f;
+  p.scale = __uint_as_float(sb) * 0.5f;
+  p.inv = p.scale > 0.f ? approx_rcp(p.scale) : 0.f;
   p.word = (sb >> 16) | (__float_as_uint(lo) & 0xFFFF0000u);
+  if (!(fabsf(lo) < INFINITY && fabsf(hi) < INFINITY)) {  // codes 0 (of x = 0 and of NaN)
+    p.word = 0x7FFF7FFFu;
+    p.off = p.scale = p.inv = 0.f;
+  }
   return p;
 }
 
-// Code of x in exact arithmetic.  off, scale and x are bf16, so -off - (n+.5)
-// scale is exact in fp64 and the last addition keeps the sign of the real sum.
-__device__ __forceinline__ uint32_t exact_code(float x, const Params& p) {
-  if (!(p.scale > 0.f)) return 0u;
-  const double q = ((double)x - (double)p.off) / (double)p.scale;
-  int n = (int)q;  // q in [0, 15]
-  n = max(0, min(n, 14));
-  // the border nearest to q is n + 0.5 for n = floor(q)
-  const double d = (double)x + (-(double)p.off - ((double)n + 0.5) * (double)p.scale);
-  return d > 0.0 ? n + 1 : (d < 0.0 ? n : n + (n & 1));
-}
-
-// Eight values (four bf16 pairs) to a code word.
-__device__ __forceinline__ uint32_t quantise8(const uint32_t (&w)[4], const Params& p) {
-  constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: rounds to an integer
-  float c[8], far = 0.f;
-#pragma unroll
-  for (int n = 0; n < 8; ++n) {
-    const float x = (n & 1) ? bf16_hi(w[n >> 1]) : bf16_lo(w[n >> 1]);
-    const float q = fmaf(x, p.k1, p.k0);
-    c[n] = __fsub_rn(__fadd_rn(q, kMagic), kMagic);
-    far = fmaxf(far, fabsf(q - c[n]));
-  }
-  if (far < 0.5f - p.tol) {
-    const float lo = fmaf(c[3], 4096.f, fmaf(c[2], 256.f, fmaf(c[1], 16.f, c[0])));
-    const float hi = fmaf(c[7], 4096.f, fmaf(c[6], 256.f, fmaf(c[5], 16.f, c[4])));
-    return (uint32_t)__float2uint_rz(lo) | ((uint32_t)__float2uint_rz(hi) << 16);
-  }
+// Codes of eight values in exact arithmetic: off, scale and x are bf16 halves, so
+// -off - (n + .5) scale is exact in fp64 and the last addition keeps the sign of
+// the real sum.
+__device__ __noinline__ uint32_t mend_codes(uint4 v, float off, float scale) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
   uint32_t out = 0;
-  if (p.word == 0x7FFF7FFFu) return out;
-#pragma unroll 1
-  for (int n = 0; n < 8; ++n) {
-    const uint32_t pair = n < 4 ? (n < 2 ? w[0] : w[1]) : (n < 6 ? w[2] : w[3]);
-    out |= exact_code((n & 1) ? bf16_hi(pair) : bf16_lo(pair), p) << (4 * n);
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t pair = i < 4 ? (i < 2 ? w[0] : w[1]) : (i < 6 ? w[2] : w[3]);
+    const double x = 0.5 * (double)((i & 1) ? bf16_hi(pair) : bf16_lo(pair));
+    const int n = max(0, min((int)((x - (double)off) / (double)scale), 14));
+    const double d = x + (-(double)off - ((double)n + 0.5) * (double)scale);
+    out |= (uint32_t)(d > 0.0 ? n + 1 : (d < 0.0 ? n : n + (n & 1))) << (4 * i);
   }
   return out;
+}
+
+// Eight values (four bf16 pairs) to a code word.  With d = x - off, the quotient
+// from the reciprocal and one correction is an exact half wherever d / scale is
+// one, so rounding it to even is right on every border that d reaches exactly;
+// and c is right whenever the remainder d - c * scale, which the fused
+// multiply-add forms exactly, is at most half a step.  What is left is mended: a
+// quotient next to a border, and a border that d reached only by rounding (|x|
+// far below |off|; a zero among the values counts as one, which costs time only).
+__device__ __forceinline__ uint32_t quantise8(const uint32_t (&w)[4], const Params& p) {
+  constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: rounds to an integer
+  const uint64_t off2 = f2_pack(-p.off, -p.off), inv2 = f2_pack(p.inv, p.inv);
+  const uint64_t neg_scale2 = f2_pack(-p.scale, -p.scale), half2 = f2_pack(0.5f, 0.5f);
+  const uint64_t magic2 = f2_pack(kMagic, kMagic);
+  float c[8], far = 0.f;
+#pragma unroll
+  for (int n = 0; n < 8; n += 2) {  // two elements an instruction
+    const uint64_t x = f2_pack(bf16_lo(w[n >> 1]), bf16_hi(w[n >> 1]));
+    const uint64_t d = f2_fma(x, half2, off2);
+    uint64_t q = f2_mul(d, inv2);
+    q = f2_fma(f2_fma(q, neg_scale2, d), inv2, q);
+    const uint64_t r = f2_sub(f2_add(q, magic2), magic2);
+    f2_unpack(r, c[n], c[n + 1]);
+    float r0, r1;
+    f2_unpack(f2_fma(r, neg_scale2, d), r0, r1);
+    far = fmax3(far, fabsf(r0), fabsf(r1));
+  }
+  const float half = 0.5f * p.scale;
+  const bool tiny = p.inv == INFINITY;  // a scale whose reciprocal overflows
+  if ((far >= half && p.scale > 0.f) || tiny) {
+    bool mend = far > half || tiny;
+    const __nv_bfloat162 least =
+        __hmin2(__hmin2(as_bf162(w[0] & 0x7FFF7FFFu), as_bf162(w[1] & 0x7FFF7FFFu)),
+                __hmin2(as_bf162(w[2] & 0x7FFF7FFFu), as_bf162(w[3] & 0x7FFF7FFFu)));
+    mend |= fminf(bf16_lo(as_u32(least)), bf16_hi(as_u32(least))) <
+            fabsf(p.off) * 1.220703125e-4f;  // 2^-13 of half the offset
+    if (mend) return mend_codes(make_uint4(w[0], w[1], w[2], w[3]), p.off, p.scale);
+  }
+  const float lo = fmaf(c[3], 4096.f, fmaf(c[2], 256.f, fmaf(c[1], 16.f, c[0])));
+  const float hi = fmaf(c[7], 4096.f, fmaf(c[6], 256.f, fmaf(c[5], 16.f, c[4])));
+  return __float2uint_rz(lo) | (__float2uint_rz(hi) << 16);
 }
 
 // Packed row r: its sequence b and absolute index, or b = -1 for a row of no
@@ -143,7 +169,9 @@ struct RowAt {
 };
 __device__ __forceinline__ RowAt locate(int r, int T, const int* cu, const int* t0, int B,
                                         long long cap) {
+  // with one new token a sequence, row r is sequence r's
   int lo = 0, hi = B - 1;
+  if (r < B && __ldg(cu + r) <= r && r < __ldg(cu + r + 1)) lo = hi = r;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
     if (__ldg(cu + mid) <= r) lo = mid;
@@ -157,7 +185,7 @@ __device__ __forceinline__ RowAt locate(int r, int T, const int* cu, const int* 
   at.pos = first + (r - a);
   return at;
 }
-// The packed offsets as a whole, by the first block: a fault is reported once.
+// The packed offsets as a whole, by one block.
 __device__ __forceinline__ void check_offsets(int T, const int* cu, const int* t0, int B,
                                               long long cap) {
   bool bad = false;
@@ -176,54 +204,89 @@ __global__ void __launch_bounds__(kThreads) append_kernel(
   using TL = Tile<D>;
   constexpr int kLanes = D / 16;  // lanes of a row
   const long long cap = (long long)pg.max_blocks * pg.block_rows;
-  if (blockIdx.x == 0 && blockIdx.y == 0) check_offsets(T, cu, t0, B, cap);
+  if (blockIdx.x == gridDim.x - 1) {  // a block of its own, beside the work
+    if (blockIdx.y == 0) check_offsets(T, cu, t0, B, cap);
+    return;
+  }
   const int i = threadIdx.x % kLanes;
   const int row = blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes;
+  // this head's rows, fetched one head ahead
+  uint4 x0 = {}, x1 = {}, y0 = {}, y1 = {};
+  auto load = [&](int h) {
+    const size_t from = ((size_t)row * pg.Hkv + h) * D + 8 * i;
+    x0 = __ldg(reinterpret_cast<const uint4*>(k_new + from));
+    x1 = __ldg(reinterpret_cast<const uint4*>(k_new + from + D / 2));
+    y0 = __ldg(reinterpret_cast<const uint4*>(v_new + from));
+    y1 = __ldg(reinterpret_cast<const uint4*>(v_new + from + D / 2));
+  };
+  const int h0 = blockIdx.y * heads_per_cta, h1 = min(h0 + heads_per_cta, pg.Hkv);
+  if (row < T) load(h0);
   RowAt at{-1, 0};
   if (row < T) at = locate(row, T, cu, t0, B, cap);
   const int pos = at.pos % s;
-  float c1[8], c2[8], s1[8], s2[8];
+  // cos and sin of two angles each, in two parts: the thread's own, kept in
+  // shared memory, which leaves registers for more warps
+  __shared__ ulonglong2 turn[4][2][kThreads];
   if (at.b >= 0) {
 #pragma unroll
-    for (int n = 0; n < 8; ++n) {
-      double c, sn;
-      sincos64((double)pos * theta.v[8 * i + n], c, sn);
-      split16(c, c1[n], c2[n]);
-      split16(sn, s1[n], s2[n]);
+    for (int n = 0; n < 4; ++n) {
+      float ch[2], cl[2], sh[2], sl[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        double c, sn;
+        sincos64((double)pos * theta.v[8 * i + 2 * n + u], c, sn);
+        split16(c, ch[u], cl[u]);
+        split16(sn, sh[u], sl[u]);
+      }
+      turn[n][0][threadIdx.x] = make_ulonglong2(f2_pack(ch[0], ch[1]), f2_pack(cl[0], cl[1]));
+      turn[n][1][threadIdx.x] = make_ulonglong2(f2_pack(sh[0], sh[1]), f2_pack(sl[0], sl[1]));
     }
   }
-  const int h0 = blockIdx.y * heads_per_cta, h1 = min(h0 + heads_per_cta, pg.Hkv);
+  // the row's place in the tile of head 0
+  uint8_t* tile0 = nullptr;
+  if (at.b >= 0) {
+    tile0 = tile_of<D>(pg, at.b, at.pos, 0);
+    if (tile0 == nullptr) {
+      if (i == 0 && blockIdx.y == 0) report_error(kDevBadArg, 205);
+      at.b = -1;
+    }
+  }
+  const int r = at.pos % kTileKeys;
+  const size_t head_bytes = (size_t)(pg.block_rows / kTileKeys) * TL::kBytes;
   const unsigned lanes = 0xFFFFFFFFu;
   for (int h = h0; h < h1; ++h) {
     uint32_t k[2][4] = {}, v[2][4] = {};
     const size_t src = ((size_t)row * pg.Hkv + h) * D + 8 * i;
     if (at.b >= 0) {
-      const uint4 x0 = __ldg(reinterpret_cast<const uint4*>(k_new + src));
-      const uint4 x1 = __ldg(reinterpret_cast<const uint4*>(k_new + src + D / 2));
-      const uint4 y0 = __ldg(reinterpret_cast<const uint4*>(v_new + src));
-      const uint4 y1 = __ldg(reinterpret_cast<const uint4*>(v_new + src + D / 2));
       v[0][0] = y0.x, v[0][1] = y0.y, v[0][2] = y0.z, v[0][3] = y0.w;
       v[1][0] = y1.x, v[1][1] = y1.y, v[1][2] = y1.z, v[1][3] = y1.w;
       const uint32_t a[4] = {x0.x, x0.y, x0.z, x0.w}, b[4] = {x1.x, x1.y, x1.z, x1.w};
+      if (h + 1 < h1) load(h + 1);
       uint32_t again = 0;  // elements next to a border, by pair
 #pragma unroll
-      for (int n = 0; n < 8; n += 2) {
-        float o0[2], o1[2];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const float p = u ? bf16_hi(a[n / 2]) : bf16_lo(a[n / 2]);
-          const float q = u ? bf16_hi(b[n / 2]) : bf16_lo(b[n / 2]);
-          const int m = n + u;
-          // products with the 16-bit parts are exact in fp32
-          o0[u] = fmaf(p, c1[m], -(q * s1[m])) + fmaf(p, c2[m], -(q * s2[m]));
-          o1[u] = fmaf(q, c1[m], p * s1[m]) + fmaf(q, c2[m], p * s2[m]);
-          const float tiny = (fabsf(p) + fabsf(q)) * 1e-11f;
-          if (near_bf16_border(o0[u], fmaf(fabsf(o0[u]), 2.4e-7f, tiny)) ||
-              near_bf16_border(o1[u], fmaf(fabsf(o1[u]), 2.4e-7f, tiny)))
-            again |= 1u << m;
-        }
-        k[0][n / 2] = pack_bf16(o0[0], o0[1]);
-        k[1][n / 2] = pack_bf16(o1[0], o1[1]);
+      for (int n = 0; n < 4; ++n) {  // two elements an instruction
+        const uint64_t p2 = f2_pack(bf16_lo(a[n]), bf16_hi(a[n]));
+        const uint64_t q2 = f2_pack(bf16_lo(b[n]), bf16_hi(b[n]));
+        const uint64_t n2 = f2_pack(bf16_lo(b[n] ^ 0x80008000u), bf16_hi(b[n] ^ 0x80008000u));
+        const ulonglong2 c = turn[n][0][threadIdx.x], sn = turn[n][1][threadIdx.x];
+        // products with the 16-bit parts are exact in fp32
+        const uint64_t o0 = f2_add(f2_fma(p2, c.x, f2_mul(n2, sn.x)),
+                                   f2_fma(p2, c.y, f2_mul(n2, sn.y)));
+        const uint64_t o1 = f2_add(f2_fma(q2, c.x, f2_mul(p2, sn.x)),
+                                   f2_fma(q2, c.y, f2_mul(p2, sn.y)));
+        float y0, y1, z0, z1;
+        f2_unpack(o0, y0, y1);
+        f2_unpack(o1, z0, z1);
+        const float t0 = (fabsf(bf16_lo(a[n])) + fabsf(bf16_lo(b[n]))) * 1e-11f;
+        const float t1 = (fabsf(bf16_hi(a[n])) + fabsf(bf16_hi(b[n]))) * 1e-11f;
+        if (near_bf16_border(y0, fmaf(fabsf(y0), 2.4e-7f, t0)) ||
+            near_bf16_border(z0, fmaf(fabsf(z0), 2.4e-7f, t0)))
+          again |= 1u << (2 * n);
+        if (near_bf16_border(y1, fmaf(fabsf(y1), 2.4e-7f, t1)) ||
+            near_bf16_border(z1, fmaf(fabsf(z1), 2.4e-7f, t1)))
+          again |= 2u << (2 * n);
+        k[0][n] = pack_bf16(y0, y1);
+        k[1][n] = pack_bf16(z0, z1);
       }
       while (again) {
         const int m = __ffs(again) - 1;
@@ -260,27 +323,56 @@ __global__ void __launch_bounds__(kThreads) append_kernel(
         mv[g] = as_u32(__hmin2_nan(as_bf162(mv[g]), as_bf162(__shfl_xor_sync(lanes, mv[g], sh))));
       }
     }
-    if (at.b < 0) continue;
-    uint8_t* tile = tile_of<D>(pg, at.b, at.pos, h);
-    if (tile == nullptr) {
-      if (i == 0 && h == h0) report_error(kDevBadArg, 205);
-      continue;
-    }
-    const int r = at.pos % kTileKeys;
+    // Every group's parameters are the same in all lanes of the row: lane j forms
+    // those of group j (keys first), the others take them from it.
+    const int j = i % (2 * TL::kGroups);
+    const Params own = make_params(j < TL::kGroups ? mk[j % TL::kGroups] : mv[j % TL::kGroups]);
+    uint8_t* tile = tile0 + h * head_bytes;
+    if (at.b >= 0 && i < 2 * TL::kGroups)
+      *reinterpret_cast<uint32_t*>(tile + (i < TL::kGroups ? TL::k_param(r, i)
+                                                           : TL::v_param(r, i - TL::kGroups))) =
+          own.word;
 #pragma unroll
-    for (int g = 0; g < TL::kGroups; ++g) {
-      const Params pk = make_params(mk[g]), pv = make_params(mv[g]);
-      if (i == g) {
-        *reinterpret_cast<uint32_t*>(tile + TL::k_param(r, g)) = pk.word;
-        *reinterpret_cast<uint32_t*>(tile + TL::v_param(r, g)) = pv.word;
-      }
+    for (int g = 0; g < 2 * TL::kGroups; ++g) {
+      Params p;
+      p.off = __shfl_sync(lanes, own.off, g, kLanes);
+      p.scale = __shfl_sync(lanes, own.scale, g, kLanes);
+      p.inv = __shfl_sync(lanes, own.inv, g, kLanes);
+      const int gr = g % TL::kGroups;
+      const bool key = g < TL::kGroups;
 #pragma unroll
-      for (int half = g; half < 2; half += TL::kGroups) {
+      for (int half = gr; half < 2; half += TL::kGroups) {
         const int word = D == 128 ? i : i + 4 * half;
-        *reinterpret_cast<uint32_t*>(tile + TL::k_word(r, g, word)) = quantise8(k[half], pk);
-        *reinterpret_cast<uint32_t*>(tile + TL::v_word(r, g, word)) = quantise8(v[half], pv);
+        const uint32_t codes = quantise8(key ? k[half] : v[half], p);
+        if (at.b >= 0)
+          *reinterpret_cast<uint32_t*>(tile + (key ? TL::k_word(r, gr, word)
+                                                   : TL::v_word(r, gr, word))) = codes;
       }
     }
+  }
+}
+
+// The eight values of a code word as bf16 pairs: code * scale + offset in fp32,
+// where it is exact unless the offset is over 2^11 steps away, rounded once.  A
+// nibble masked in place under the exponent of 2^23 is 2^23 + c * 16^n, so the
+// code comes out by a subtraction and its place goes into the scale.
+__device__ __forceinline__ void dequantise8(uint32_t w, uint32_t param, uint32_t (&out)[4]) {
+  const float scale = bf16_lo(param), off = bf16_hi(param);
+  const uint64_t off2 = f2_pack(off, off), base2 = f2_pack(8388608.f, 8388608.f);
+  const uint64_t s01 = f2_pack(scale, scale * 0.0625f);
+  const uint64_t s23 = f2_pack(scale * 0.00390625f, scale * 0.000244140625f);
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const uint32_t u = w >> (16 * j);
+    const uint64_t c01 = f2_pack(__uint_as_float((u & 0xFu) | 0x4B000000u),
+                                 __uint_as_float((u & 0xF0u) | 0x4B000000u));
+    const uint64_t c23 = f2_pack(__uint_as_float((u & 0xF00u) | 0x4B000000u),
+                                 __uint_as_float((u & 0xF000u) | 0x4B000000u));
+    float a, b;
+    f2_unpack(f2_fma(f2_sub(c01, base2), s01, off2), a, b);
+    out[2 * j] = pack_bf16(a, b);
+    f2_unpack(f2_fma(f2_sub(c23, base2), s23, off2), a, b);
+    out[2 * j + 1] = pack_bf16(a, b);
   }
 }
 
@@ -297,7 +389,10 @@ __global__ void __launch_bounds__(kThreads) read_kernel(
   const long long cap = out_rows > 0
                             ? min((long long)pg.max_blocks * pg.block_rows, (long long)out_rows)
                             : (long long)pg.max_blocks * pg.block_rows;
-  if (blockIdx.x == 0) check_offsets(T, cu, t0, B, cap);
+  if (blockIdx.x == gridDim.x - 1) {
+    check_offsets(T, cu, t0, B, cap);
+    return;
+  }
   const long long gid = (long long)blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes;
   const int i = threadIdx.x % kLanes;
   if (gid >= (long long)T * pg.Hkv) return;
@@ -324,13 +419,8 @@ __global__ void __launch_bounds__(kThreads) read_kernel(
     const uint32_t pk = __ldg(reinterpret_cast<const uint32_t*>(tile + TL::k_param(r, g)));
     const uint32_t pv = __ldg(reinterpret_cast<const uint32_t*>(tile + TL::v_param(r, g)));
     uint32_t k[4], v[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float a0 = (float)((wk >> (8 * j)) & 15u), a1 = (float)((wk >> (8 * j + 4)) & 15u);
-      const float b0 = (float)((wv >> (8 * j)) & 15u), b1 = (float)((wv >> (8 * j + 4)) & 15u);
-      k[j] = pack_bf16(fmaf(a0, bf16_lo(pk), bf16_hi(pk)), fmaf(a1, bf16_lo(pk), bf16_hi(pk)));
-      v[j] = pack_bf16(fmaf(b0, bf16_lo(pv), bf16_hi(pv)), fmaf(b1, bf16_lo(pv), bf16_hi(pv)));
-    }
+    dequantise8(wk, pk, k);
+    dequantise8(wv, pv, v);
     *reinterpret_cast<uint4*>(Ko + dst + half * (D / 2)) = make_uint4(k[0], k[1], k[2], k[3]);
     *reinterpret_cast<uint4*>(Vo + dst + half * (D / 2)) = make_uint4(v[0], v[1], v[2], v[3]);
   }
@@ -346,7 +436,7 @@ cudaError_t launch_append_t(const void* k_new, const void* v_new, const Pages& p
   int hpc = pg.Hkv;
   while (hpc > 1 && (long long)gx * ((pg.Hkv + hpc - 1) / hpc) < 148 * 4) hpc = (hpc + 1) / 2;
   const unsigned gy = (unsigned)((pg.Hkv + hpc - 1) / hpc);
-  append_kernel<D><<<dim3(gx, gy), kThreads, 0, stream>>>(
+  append_kernel<D><<<dim3(gx + 1, gy), kThreads, 0, stream>>>(
       static_cast<const __nv_bfloat16*>(k_new), static_cast<const __nv_bfloat16*>(v_new), pg, cu,
       t0, B, T, s, hpc, make_theta(D, base));
   return cudaGetLastError();
@@ -357,7 +447,7 @@ cudaError_t launch_read_t(void* K, void* V, const Pages& pg, const int* cu, cons
                           int T, int out_rows, cudaStream_t stream) {
   constexpr int kRows = kThreads / (D / 16);
   const unsigned grid = (unsigned)(((long long)T * pg.Hkv + kRows - 1) / kRows);
-  read_kernel<D><<<grid, kThreads, 0, stream>>>(static_cast<__nv_bfloat16*>(K),
+  read_kernel<D><<<grid + 1, kThreads, 0, stream>>>(static_cast<__nv_bfloat16*>(K),
                                                 static_cast<__nv_bfloat16*>(V), pg, cu, t0, B, T,
                                                 out_rows);
   return cudaGetLastError();

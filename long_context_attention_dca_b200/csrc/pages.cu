@@ -400,7 +400,8 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads,
 constexpr int kChunk = 32 << 10;
 constexpr int kCopyThreads = 256;
 
-__global__ void __launch_bounds__(kCopyThreads) copy_pages(const __grid_constant__ PoolList pools,
+template <int N>
+__global__ void __launch_bounds__(kCopyThreads) copy_pages(const __grid_constant__ Pools<N> pools,
                                                            int R, Work w) {
   const int n = __ldcg(w.head + 1);
   const long long items = (long long)n * pools.items;
@@ -445,7 +446,16 @@ cudaError_t launch_copies(PoolList& pools, int R, const Work& w, cudaStream_t st
     pools.items += d.items;
   }
   if (pools.items == 0) return cudaSuccess;
-  copy_pages<<<148 * 6, kCopyThreads, 0, stream>>>(pools, R, w);
+  // The list travels with the launch, at a cost by its size: two sizes of it.
+  if (pools.n <= 16) {
+    Pools<16> few;
+    few.items = pools.items;
+    few.n = pools.n;
+    for (int j = 0; j < pools.n; ++j) few.p[j] = pools.p[j];
+    copy_pages<16><<<148 * 6, kCopyThreads, 0, stream>>>(few, R, w);
+  } else {
+    copy_pages<kMaxPools><<<148 * 6, kCopyThreads, 0, stream>>>(pools, R, w);
+  }
   return cudaGetLastError();
 }
 

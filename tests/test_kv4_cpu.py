@@ -184,11 +184,20 @@ def test_tile_and_workspace_sizes(lib):
     assert dca.dca_kv4_tile_bytes(128) == 9216 and dca.dca_kv4_tile_bytes(64) == 4608
     assert dca.dca_kv4_tile_bytes(96) == 0
     assert dca.dca_attn_decode_kv4_workspace(0, 8, 1, 128, 64) == 0
-    one = dca.dca_attn_decode_kv4_workspace(1, 8, 1, 128, 64)
-    assert one == 2 * 8 * 130 * 4  # one unit of one tile: a slot for either, 8 heads each
+    # a slot of 8 heads x (D + 2) floats for every unit (sequence, kv head, 8
+    # query heads) and every share; a share is four tiles, a unit its tiles and
+    # 12 more, and there are 3 shares an SM at most unless one passes 512 tiles
+    def slots(B, Hkv, groups, Tcap):
+        units = B * Hkv * groups
+        tiles = units * (-(-Tcap // 64) + 12)
+        return units + max(1, min(tiles // 4, max(148 * 3, -(-tiles // 512))))
+
+    for B, Hq, Hkv, D, Tcap in ((1, 8, 1, 128, 64), (1, 8, 1, 64, 129), (16, 64, 8, 128, 65536),
+                                (3, 20, 2, 64, 1000), (64, 64, 64, 128, 1 << 20)):
+        want = slots(B, Hkv, -(-(Hq // Hkv) // 8), Tcap) * 8 * (D + 2) * 4
+        assert dca.dca_attn_decode_kv4_workspace(B, Hq, Hkv, D, Tcap) == want
     assert dca.dca_attn_decode_kv4_workspace(1, 8, 3, 128, 64) == 0
     assert dca.dca_attn_decode_kv4_workspace(1, 8, 1, 128, 0) == 0
-    assert dca.dca_attn_decode_kv4_workspace(1, 8, 1, 64, 128) == 3 * 8 * 66 * 4
     assert dca.dca_pages_workspace(0, 1, 1) > 0 and dca.dca_pages_workspace(-1, 1, 1) == 0
     assert dca.dca_pages_workspace(4, 0, 10) == 0 and dca.dca_pages_workspace(4, 3, 0) == 0
 
