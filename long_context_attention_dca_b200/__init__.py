@@ -13,6 +13,7 @@ Build the library with ``python -m long_context_attention_dca_b200.build``.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -651,6 +652,7 @@ def dca_kv4_read_paged(pool, block_table, cu_seqlens, t0, T, D, K=None, V=None):
     return K, V
 
 
+@functools.lru_cache(maxsize=256)
 def dca_attn_decode_kv4_workspace(B: int, Hq: int, Hkv: int, D: int, Tcap: int) -> int:
     return int(lib().dca_attn_decode_kv4_workspace(B, Hq, Hkv, D, Tcap))
 
@@ -676,14 +678,14 @@ def dca_attn_decode_kv4_paged(q, pool, block_table, t, s, c, base=10000.0, scale
         if O.shape != q.shape:
             raise DcaError(1, "O must have the shape of q")
     if LSE is None:
-        LSE = torch.empty((B, Hq), dtype=torch.float32, device=dev)
+        LSE = q.new_empty((B, Hq), dtype=torch.float32)
     else:
         _need(LSE, "LSE", torch.float32, 2)
         if tuple(LSE.shape) != (B, Hq):
             raise DcaError(1, f"LSE must be {(B, Hq)}, got {tuple(LSE.shape)}")
     if workspace is None:
-        workspace = _workspace(dca_attn_decode_kv4_workspace(B, Hq, Hkv, D,
-                                                             max_blocks * block_rows), dev)
+        workspace = q.new_empty(-(-dca_attn_decode_kv4_workspace(
+            B, Hq, Hkv, D, max_blocks * block_rows) // 2))
     _same_device(dev, pool, block_table, t, O, LSE, workspace)
     _call("dca_attn_decode_kv4_paged", dev, q.data_ptr(), pool.data_ptr(),
           block_table.data_ptr(), max_blocks, block_rows, num_blocks, t.data_ptr(), O.data_ptr(),
@@ -740,6 +742,7 @@ def _page_out(name, x, like):
     return x
 
 
+@functools.lru_cache(maxsize=256)
 def dca_pages_workspace(B: int, max_blocks: int, num_blocks: int) -> int:
     return int(lib().dca_pages_workspace(B, max_blocks, num_blocks))
 

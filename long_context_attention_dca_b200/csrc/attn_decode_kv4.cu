@@ -24,6 +24,8 @@
 // and the update of O are paid once per 64 keys of a warp.  The sequence's
 // tiles are shared out evenly on the device from t[b], whatever the cache's
 // capacity.  Kernel 2 merges the shares.
+#include <atomic>
+
 #include "dca_common.cuh"
 #include "dca_index.cuh"
 #include "dca_kernels.cuh"
@@ -176,6 +178,7 @@ __global__ void __launch_bounds__(kDecodeThreads, kCtasPerSm) decode_kernel(
   volatile int* bad_page = abort_flag + 1;
   uint32_t* places = reinterpret_cast<uint32_t*>(bars + SM::kBars);
 
+  cudaTriggerProgrammaticLaunchCompletion();  // the merge may take its places
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = Hq / pg.Hkv, per_seq = pg.Hkv * n_hg;
   const int tpb = pg.block_rows / kTileKeys;
@@ -630,75 +633,72 @@ __global__ void __launch_bounds__(kDecodeThreads, kCtasPerSm) decode_kernel(
 }
 
 // O = sum_p e^{m_p - m} O_p / sum_p e^{m_p - m} l_p over the partial results of
-// a unit, LSE = m + ln(sum): one block a (head, sequence), four rows of D/4
-// threads over the partials in turn.
+// a unit, LSE = m + ln(sum).  One block a (head, sequence), its eight warps over
+// the partials in turn, a row of D a warp.  It starts beside the decode kernel,
+// finds its place from t and waits for the results.
+constexpr int kMergeThreads = 256;
+
 template <int D>
-__global__ void __launch_bounds__(D) decode_merge(const float* __restrict__ Opart,
-                                                  const float2* __restrict__ MLpart,
-                                                  const int* __restrict__ t,
-                                                  __nv_bfloat16* __restrict__ O,
-                                                  float* __restrict__ LSE, int B, int Hq, int Hkv,
-                                                  int n_hg, long long cap, int grid_shares) {
-  __shared__ float4 part[4][D / 4];
-  __shared__ float stat[2];
-  __shared__ long long sums[D / 32];
-  const int h = blockIdx.x, b = blockIdx.y, d = threadIdx.x;
+__global__ void __launch_bounds__(kMergeThreads) decode_merge(
+    const float* __restrict__ Opart, const float2* __restrict__ MLpart,
+    const int* __restrict__ t, __nv_bfloat16* __restrict__ O, float* __restrict__ LSE, int B,
+    int Hq, int Hkv, int n_hg, long long cap, int grid_shares) {
+  constexpr int kW = kMergeThreads / 32, kEach = D / 32;
+  __shared__ float part[kW][D];
+  __shared__ float2 stat[kW];
+  __shared__ long long sums[kW];
+  const int h = blockIdx.x, b = blockIdx.y, d = threadIdx.x, warp = d >> 5, lane = d & 31;
   const int tb = __ldg(t + b);
   const size_t row = (size_t)b * Hq + h;
-  if (tb < 0 || tb >= cap) {
-    O[row * D + d] = __float2bfloat16_rn(__int_as_float(0x7fc00000));
-    if (d == 0) LSE[row] = __int_as_float(0x7fc00000);
-    return;
-  }
   const int G = Hq / Hkv, per_seq = Hkv * n_hg;
   const int unit = h / G * n_hg + h % G / kHeads, hh = h % G % kHeads;
   const long long all = spans_before(t, B, cap, sums) * per_seq;
-  const Split split{all, share_count(all, grid_shares)};
   const int tiles = tiles_of(tb, cap);
   const long long g0 =
       spans_before(t, b, cap, sums) * per_seq + (long long)unit * (tiles + kSetup) + kSetup;
+  cudaGridDependencySynchronize();
+  if (tiles == 0) {
+    if (d < D) O[row * D + d] = __float2bfloat16_rn(__int_as_float(0x7fc00000));
+    if (d == 0) LSE[row] = __int_as_float(0x7fc00000);
+    return;
+  }
+  const Split split{all, share_count(all, grid_shares)};
   const long long c0 = share_of(split, g0);
   const int n = (int)(share_of(split, g0 + tiles - 1) - c0) + 1;
   const size_t slot0 = ((size_t)b * per_seq + unit + c0) * kHeads + hh;
-  const float2* ml = MLpart + slot0;
-  if (d < 32) {
-    float M = -INFINITY;
-    for (int p = d; p < n; p += 32) M = fmaxf(M, ml[(size_t)p * kHeads].x);
-#pragma unroll
-    for (int sh = 16; sh >= 1; sh >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, sh));
-    const float mu = M == -INFINITY ? 0.f : M;
-    float l = 0.f;
-    for (int p = d; p < n; p += 32) {
-      const float2 v = ml[(size_t)p * kHeads];
-      l += fast_exp2(v.x - mu) * v.y;
-    }
-#pragma unroll
-    for (int sh = 16; sh >= 1; sh >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, sh);
-    if (d == 0) {
-      stat[0] = mu;
-      stat[1] = l;
-    }
-  }
-  __syncthreads();
-  const float M = stat[0], l = stat[1];
-  const int lane = d % (D / 4), first = d / (D / 4);
-  const float4* src = reinterpret_cast<const float4*>(Opart) + slot0 * (D / 4) + lane;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  // every warp its own partials' sum, relative to their own maximum
+  float m = -INFINITY, l = 0.f, acc[kEach] = {};
 #pragma unroll 4
-  for (int p = first; p < n; p += 4) {
-    const float f = fast_exp2(ml[(size_t)p * kHeads].x - M);
-    const float4 v = src[(size_t)p * kHeads * (D / 4)];
-    acc.x = fmaf(f, v.x, acc.x);
-    acc.y = fmaf(f, v.y, acc.y);
-    acc.z = fmaf(f, v.z, acc.z);
-    acc.w = fmaf(f, v.w, acc.w);
+  for (int p = warp; p < n; p += kW) {
+    const size_t slot = slot0 + (size_t)p * kHeads;
+    const float2 ml = MLpart[slot];
+    float v[kEach];
+    if (D == 128) *reinterpret_cast<float4*>(v) = reinterpret_cast<const float4*>(Opart + slot * D)[lane];
+    else *reinterpret_cast<float2*>(v) = reinterpret_cast<const float2*>(Opart + slot * D)[lane];
+    const float mn = fmaxf(m, ml.x), mu = mn == -INFINITY ? 0.f : mn;
+    const float old = fast_exp2(m - mu), now = fast_exp2(ml.x - mu);
+    m = mn;
+    l = l * old + ml.y * now;
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) acc[e] = acc[e] * old + v[e] * now;
   }
-  part[first][lane] = acc;
+#pragma unroll
+  for (int e = 0; e < kEach; ++e) part[warp][lane * kEach + e] = acc[e];
+  if (lane == 0) stat[warp] = make_float2(m, l);
   __syncthreads();
-  const float* col = reinterpret_cast<const float*>(part);
-  const float sum = (col[d] + col[D + d]) + (col[2 * D + d] + col[3 * D + d]);
-  O[row * D + d] = __float2bfloat16_rn(sum / l);
-  if (d == 0) LSE[row] = (M + log2f(l)) * 0.69314718055994530942f;
+  if (d >= D) return;
+  float M = -INFINITY, sum = 0.f, total = 0.f;
+#pragma unroll
+  for (int w = 0; w < kW; ++w) M = fmaxf(M, stat[w].x);
+  const float mu = M == -INFINITY ? 0.f : M;
+#pragma unroll
+  for (int w = 0; w < kW; ++w) {
+    const float f = fast_exp2(stat[w].x - mu);
+    total += f * stat[w].y;
+    sum += f * part[w][d];
+  }
+  O[row * D + d] = __float2bfloat16_rn(sum / total);
+  if (d == 0) LSE[row] = (mu + log2f(total)) * 0.69314718055994530942f;
 }
 
 template <int D>
@@ -713,17 +713,23 @@ cudaError_t launch_decode_t(const void* q, const Pages& pg, const int* t, void* 
   float2* MLpart = reinterpret_cast<float2*>(Opart + slots * D);
   auto kern = decode_kernel<D>;
   constexpr int smem = DecodeSmem<D>::kTotal;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // once a device: the attribute stays with the function there
+  static std::atomic<unsigned long long> set{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess && (dev >= 64 || !(set.load() >> dev & 1))) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess && dev < 64) set.fetch_or(1ull << dev);
+  }
   if (e != cudaSuccess) return e;
   kern<<<shares, kDecodeThreads, smem, stream>>>(
       static_cast<const __nv_bfloat16*>(q), pg, t, Opart, MLpart, B, Hq, s, c,
       scale * 1.4426950408889634f, n_hg, make_theta(D, base));
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  decode_merge<D><<<dim3(Hq, B), D, 0, stream>>>(Opart, MLpart, t,
-                                                 static_cast<__nv_bfloat16*>(O), LSE, B, Hq,
-                                                 pg.Hkv, n_hg, cap, shares);
-  return cudaGetLastError();
+  return launch_early(decode_merge<D>, dim3(Hq, B), kMergeThreads, stream,
+                      static_cast<const float*>(Opart), static_cast<const float2*>(MLpart), t,
+                      static_cast<__nv_bfloat16*>(O), LSE, B, Hq, pg.Hkv, n_hg, cap, shares);
 }
 
 }  // namespace kv4

@@ -190,6 +190,24 @@ cudaError_t launch_wait_timeout(int deadline_us, cudaStream_t stream);
 cudaError_t launch_index_map(int L, int s, int c, int* qpos, int* kpos, signed char* piece,
                              cudaStream_t stream);
 
+// Launch a kernel that may take its place on the SMs while the kernel before it
+// runs (once that has triggered or ended) and waits for the other's results
+// itself (cudaGridDependencySynchronize).
+template <typename... P, typename... A>
+inline cudaError_t launch_early(void (*kern)(P...), dim3 grid, int threads, cudaStream_t stream,
+                         A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 // Driver entry point for building TMA tensor maps (resolved once).
 bool encode_tensor_map(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, int rank,
                        const uint64_t* dims, const uint64_t* strides_bytes, const uint32_t* box,

@@ -8,25 +8,35 @@
 // shows in the outputs.
 //
 // Each runs as two kernels.  The plan is integer work over B * max_blocks
-// entries and num_blocks counts with a handful of dependent phases: one
-// cluster of 8 CTAs, whose hardware barrier separates the phases, holds it in
-// one launch.  The copies move the bytes, a chunk a block at a time, from a
-// list whose length stays on the device; they are bound by memory bandwidth.
+// entries and num_blocks counts with a handful of dependent phases.  A state
+// that fits one CTA's shared memory is planned there by that CTA; a larger one
+// by a cluster of 8 CTAs in global memory, whose hardware barrier separates the
+// phases.  The copies move the bytes, a chunk a block at a time, from a list
+// whose length stays on the device; they are bound by memory bandwidth.
 #include "dca_common.cuh"
 #include "dca_kernels.cuh"
 
 namespace dca {
 namespace pages {
 
-constexpr int kCluster = 8;
 constexpr int kPlanThreads = 1024;
-constexpr int kAll = kCluster * kPlanThreads;
 constexpr int kNone = 0x7FFFFFFF;
 
-__device__ __forceinline__ void cluster_barrier() {
-  __threadfence();
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+// C CTAs plan together.  Working arrays written by one and read by another are
+// read past the L1 cache; a CTA alone has them in shared memory.
+template <int C>
+__device__ __forceinline__ void phase_end() {
+  if (C == 1) {
+    __syncthreads();
+  } else {
+    __threadfence();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  }
+}
+template <int C>
+__device__ __forceinline__ int get(const int* p) {
+  return C == 1 ? *p : __ldcg(p);
 }
 __device__ __forceinline__ int pages_of(int n, int R) {
   return (int)(((long long)n + R - 1) / R);
@@ -64,50 +74,57 @@ __device__ __forceinline__ int block_scan(int v, int* warp_sums, int& total) {
 struct Part {
   int begin, end;
 };
+template <int C>
 __device__ __forceinline__ Part part_of(int n, int rank) {
-  const int per = (int)(((long long)n + kCluster - 1) / kCluster);
+  const int per = (int)(((long long)n + C - 1) / C);
   const long long a = (long long)per * rank;
   return Part{(int)min(a, (long long)n), (int)min(a + per, (long long)n)};
 }
 
-struct Work {  // workspace, all int32
-  int* head;    // [64]: 0 faults, 1 copies; 8.. per-CTA sums
+struct Work {  // all int32
+  int* out;     // [64]: 0 copies.  Always in the workspace, as the copy list:
+  int* from;    // [max(num_blocks, B)] source page
+  int* to;      //                      target page
+  int* rows;    //                      rows to copy
+  int* head;    // [64]: 0 faults, 1 copies, 2 pages wanted; 8.. per-CTA sums
   int* count;   // [num_blocks] references while the plan runs
-  int* owner;   // [num_blocks] slot that keeps a partial page
+  int* owner;   // [num_blocks] slot that keeps a partial page; a page's new index
   int* list;    // [num_blocks] free pages or holes, ascending
-  int* from;    // [max(num_blocks, B)] copy list: source page
-  int* to;      //                       target page
-  int* rows;    //                       rows to copy
   int* table;   // [B * max_blocks] the table as it came
   int* slots;   // [3][B] full pages kept, rows of the partial one, first new page
 };
 constexpr int kHead = 64;
 
+size_t list_ints(int B, int num_blocks) {
+  return kHead + 3 * (size_t)(num_blocks > B ? num_blocks : B);
+}
+__host__ __device__ inline size_t plan_ints(int B, int max_blocks, int num_blocks) {
+  return kHead + 3 * (size_t)num_blocks + (size_t)B * max_blocks + 3 * (size_t)B;
+}
 size_t work_ints(int B, int max_blocks, int num_blocks) {
-  const size_t m = (size_t)(num_blocks > B ? num_blocks : B);
-  return kHead + 3 * (size_t)num_blocks + 3 * m + (size_t)B * max_blocks + 3 * (size_t)B;
+  return list_ints(B, num_blocks) + plan_ints(B, max_blocks, num_blocks);
+}
+// A plan in one CTA's shared memory: measured at 16 x 23 entries and 153 pages,
+// 18.8 us as a cluster in global memory; see the launches below.
+constexpr size_t kAloneInts = 50000;
+
+__host__ __device__ inline void carve_plan(Work& w, int* p, int B, int max_blocks,
+                                           int num_blocks) {
+  w.head = p;
+  w.count = w.head + kHead;
+  w.owner = w.count + num_blocks;
+  w.list = w.owner + num_blocks;
+  w.table = w.list + num_blocks;
+  w.slots = w.table + (size_t)B * max_blocks;
 }
 Work carve(void* ws, int B, int max_blocks, int num_blocks) {
   const size_t m = (size_t)(num_blocks > B ? num_blocks : B);
   Work w;
-  int* p = static_cast<int*>(ws);
-  w.head = p;
-  p += kHead;
-  w.count = p;
-  p += num_blocks;
-  w.owner = p;
-  p += num_blocks;
-  w.list = p;
-  p += num_blocks;
-  w.from = p;
-  p += m;
-  w.to = p;
-  p += m;
-  w.rows = p;
-  p += m;
-  w.table = p;
-  p += (size_t)B * max_blocks;
-  w.slots = p;
+  w.out = static_cast<int*>(ws);
+  w.from = w.out + kHead;
+  w.to = w.from + m;
+  w.rows = w.to + m;
+  carve_plan(w, w.rows + m, B, max_blocks, num_blocks);
   return w;
 }
 
@@ -115,7 +132,8 @@ Work carve(void* ws, int B, int max_blocks, int num_blocks) {
 // slot src[b] (none for -1) and pages for new_len[b] rows.  Full pages are
 // shared.  A partial last page goes to the lowest slot that wants it unless it
 // is still held elsewhere; every other slot gets a copy of its rows.
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads, 1) remap_plan(
+template <int C>
+__global__ void __cluster_dims__(C, 1, 1) __launch_bounds__(kPlanThreads, 1) remap_plan(
     const int* __restrict__ src, const int* __restrict__ old_len,
     const int* __restrict__ new_len, const int* table_in, int* table_out, const int* refs_in,
     int* refs_out, int* __restrict__ info, int B, int max_blocks, int num_blocks, int R,
@@ -124,6 +142,10 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads,
   __shared__ int carry;
   const int rank = blockIdx.x, tid = threadIdx.x;
   const int gid = rank * kPlanThreads + tid;
+  constexpr int kAll = C * kPlanThreads;
+  extern __shared__ int plan_smem[];
+  if (C == 1) carve_plan(w, plan_smem, B, max_blocks, num_blocks);
+  cudaTriggerProgrammaticLaunchCompletion();  // the copies may take their places
   const long long entries = (long long)B * max_blocks;
   const long long cap = (long long)max_blocks * R;
   if (rank == 0 && tid < kHead) w.head[tid] = 0;
@@ -132,7 +154,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads,
     w.owner[p] = kNone;
   }
   for (long long e = gid; e < entries; e += kAll) w.table[e] = table_in[e];
-  cluster_barrier();
+  phase_end<C>();
 
   // drop what the slots hold; a fault anywhere refuses the whole call
   bool bad = false;
@@ -155,35 +177,35 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads,
   }
   for (int p = gid; p < num_blocks; p += kAll) bad |= refs_in[p] < 0;
   if (bad) atomicExch(w.head, 1);
-  cluster_barrier();
-  const bool fault = __ldcg(w.head) != 0;
+  phase_end<C>();
+  const bool fault = get<C>(w.head) != 0;
 
   // full pages are shared by every slot that keeps them
   if (!fault) {
     for (long long e = gid; e < entries; e += kAll) {
       const int b = (int)(e / max_blocks), i = (int)(e % max_blocks);
-      if (i < __ldcg(w.slots + b)) {
+      if (i < get<C>(w.slots + b)) {
         const int f = src[b];
-        atomicAdd(w.count + __ldcg(w.table + (size_t)f * max_blocks + i), 1);
+        atomicAdd(w.count + get<C>(w.table + (size_t)f * max_blocks + i), 1);
       }
     }
   }
-  cluster_barrier();
+  phase_end<C>();
   // partial pages that nobody holds any more go to the lowest slot
   if (!fault) {
     for (int b = gid; b < B; b += kAll) {
-      if (__ldcg(w.slots + B + b) == 0) continue;
-      const int p = __ldcg(w.table + (size_t)src[b] * max_blocks + __ldcg(w.slots + b));
-      if (__ldcg(w.count + p) == 0) atomicMin(w.owner + p, b);
+      if (get<C>(w.slots + B + b) == 0) continue;
+      const int p = get<C>(w.table + (size_t)src[b] * max_blocks + get<C>(w.slots + b));
+      if (get<C>(w.count + p) == 0) atomicMin(w.owner + p, b);
     }
   }
-  cluster_barrier();
+  phase_end<C>();
 
   // free pages in ascending order, each CTA ranking its own part
-  const Part mine = part_of(num_blocks, rank);
+  const Part mine = part_of<C>(num_blocks, rank);
   int local = 0;
   for (int p = mine.begin + tid; p < mine.end; p += kPlanThreads)
-    local += __ldcg(w.count + p) == 0 && __ldcg(w.owner + p) == kNone;
+    local += get<C>(w.count + p) == 0 && get<C>(w.owner + p) == kNone;
   int part_free;
   block_scan(local, sums, part_free);
   if (tid == 0) w.head[8 + rank] = part_free;
@@ -196,11 +218,11 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads,
       const int b = b0 + tid;
       int need = 0;
       if (b < B && !fault) {
-        const int full = __ldcg(w.slots + b), rest = __ldcg(w.slots + B + b);
+        const int full = get<C>(w.slots + b), rest = get<C>(w.slots + B + b);
         bool stays = false;
         if (rest) {
-          const int p = __ldcg(w.table + (size_t)src[b] * max_blocks + full);
-          stays = __ldcg(w.owner + p) == b;
+          const int p = get<C>(w.table + (size_t)src[b] * max_blocks + full);
+          stays = get<C>(w.owner + p) == b;
         }
         need = pages_of(new_len[b], R) - full - (stays ? 1 : 0);
       }
@@ -213,22 +235,23 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads,
     }
     if (tid == 0) w.head[2] = carry;
   }
-  cluster_barrier();
+  phase_end<C>();
 
   int before = 0, free_all = 0;
-  for (int r = 0; r < kCluster; ++r) {
-    const int n = __ldcg(w.head + 8 + r);
+  for (int r = 0; r < C; ++r) {
+    const int n = get<C>(w.head + 8 + r);
     if (r < rank) before += n;
     free_all += n;
   }
-  const int need_all = __ldcg(w.head + 2);
+  const int need_all = get<C>(w.head + 2);
   if (fault || need_all > free_all) {  // refused: the state as it came
-    for (long long e = gid; e < entries; e += kAll) table_out[e] = __ldcg(w.table + e);
+    for (long long e = gid; e < entries; e += kAll) table_out[e] = get<C>(w.table + e);
     if (refs_out != refs_in)
       for (int p = gid; p < num_blocks; p += kAll) refs_out[p] = refs_in[p];
     if (gid == 0) {
       info[0] = fault ? kNone : -(need_all - free_all);
       info[1] = 0;
+      w.out[0] = 0;
       if (fault) report_error(kDevBadArg, 209);
     }
     return;
@@ -237,8 +260,8 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads,
     const int p = p0 + tid;
     int n = 0, free = 0;
     if (p < mine.end) {
-      n = __ldcg(w.count + p);
-      const bool kept = __ldcg(w.owner + p) != kNone;
+      n = get<C>(w.count + p);
+      const bool kept = get<C>(w.owner + p) != kNone;
       if (kept) n = 1;
       free = n == 0;
     }
@@ -253,24 +276,24 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads,
     }
     before += total;
   }
-  cluster_barrier();
+  phase_end<C>();
 
   for (long long e = gid; e < entries; e += kAll) {
     const int b = (int)(e / max_blocks), i = (int)(e % max_blocks);
-    const int full = __ldcg(w.slots + b), rest = __ldcg(w.slots + B + b);
+    const int full = get<C>(w.slots + b), rest = get<C>(w.slots + B + b);
     const int n = pages_of(new_len[b], R);
     int page = -1;
     if (i < n) {
       const int* row = w.table + (size_t)max(src[b], 0) * max_blocks;
       if (i < full) {
-        page = __ldcg(row + i);
+        page = get<C>(row + i);
       } else {
-        const int tail = rest ? __ldcg(row + full) : -1;
-        const bool stays = rest && __ldcg(w.owner + tail) == b;
+        const int tail = rest ? get<C>(row + full) : -1;
+        const bool stays = rest && get<C>(w.owner + tail) == b;
         if (i == full && stays) {
           page = tail;
         } else {
-          page = __ldcg(w.list + __ldcg(w.slots + 2 * B + b) + i - full - (stays ? 1 : 0));
+          page = get<C>(w.list + get<C>(w.slots + 2 * B + b) + i - full - (stays ? 1 : 0));
           if (i == full && rest) {
             const int k = atomicAdd(w.head + 1, 1);
             w.from[k] = tail;
@@ -282,25 +305,30 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads,
     }
     table_out[e] = page;
   }
-  cluster_barrier();
+  phase_end<C>();
   if (gid == 0) {
     info[0] = free_all - need_all;
-    info[1] = __ldcg(w.head + 1);
+    info[1] = w.out[0] = get<C>(w.head + 1);
   }
 }
 
 // Pages in use (refs > 0) with an index of n or more, n their number, move to
 // the free indexes below n, both in ascending order.
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads, 1) compact_plan(
+template <int C>
+__global__ void __cluster_dims__(C, 1, 1) __launch_bounds__(kPlanThreads, 1) compact_plan(
     const int* __restrict__ len, const int* table_in, int* table_out, const int* refs_in,
     int* refs_out, int* __restrict__ moved, int* __restrict__ info, int B, int max_blocks,
     int num_blocks, int R, Work w) {
   __shared__ int sums[32];
   const int rank = blockIdx.x, tid = threadIdx.x;
   const int gid = rank * kPlanThreads + tid;
+  constexpr int kAll = C * kPlanThreads;
+  extern __shared__ int plan_smem[];
+  if (C == 1) carve_plan(w, plan_smem, B, max_blocks, num_blocks);
+  cudaTriggerProgrammaticLaunchCompletion();  // the copies may take their places
   const long long entries = (long long)B * max_blocks;
   const long long cap = (long long)max_blocks * R;
-  const Part mine = part_of(num_blocks, rank);
+  const Part mine = part_of<C>(num_blocks, rank);
   if (rank == 0 && tid < 8) w.head[tid] = 0;
   bool bad = false;
   int local = 0;
@@ -321,16 +349,17 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads,
       bad = true;
     } else if (i < pages_of(n, R)) {
       const int p = table_in[e];
-      if (p < 0 || p >= num_blocks || refs_in[p] <= 0) bad = true;
+      // (one CTA has all counts by now, past the scan's barriers)
+      if (p < 0 || p >= num_blocks || (C == 1 ? w.count[p] : refs_in[p]) <= 0) bad = true;
     }
   }
   if (max_blocks > 0)
     for (int b = gid; b < B; b += kAll) bad |= len[b] < 0 || len[b] > cap;
-  cluster_barrier();
+  phase_end<C>();
   if (bad) atomicExch(w.head, 1);
   int before = 0, live = 0;
-  for (int r = 0; r < kCluster; ++r) {
-    const int n = __ldcg(w.head + 8 + r);
+  for (int r = 0; r < C; ++r) {
+    const int n = get<C>(w.head + 8 + r);
     if (r < rank) before += n;
     live += n;
   }
@@ -341,21 +370,21 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads,
   int part_low;
   block_scan(local, sums, part_low);
   if (tid == 0) w.head[16 + rank] = part_low;
-  cluster_barrier();
-  if (__ldcg(w.head)) {
-    for (long long e = gid; e < entries; e += kAll) table_out[e] = __ldcg(w.table + e);
+  phase_end<C>();
+  if (get<C>(w.head)) {
+    for (long long e = gid; e < entries; e += kAll) table_out[e] = get<C>(w.table + e);
     if (refs_out != refs_in)
       for (int p = gid; p < num_blocks; p += kAll) refs_out[p] = refs_in[p];
     for (int p = gid; p < num_blocks; p += kAll) moved[p] = p;
     if (gid == 0) {
       info[0] = kNone;
-      info[1] = 0;
+      info[1] = w.out[0] = 0;
       report_error(kDevBadArg, 210);
     }
     return;
   }
   int low = 0;
-  for (int r = 0; r < kCluster; ++r) low += __ldcg(w.head + 16 + r);
+  for (int r = 0; r < C; ++r) low += get<C>(w.head + 16 + r);
   for (int p0 = mine.begin; p0 < mine.end; p0 += kPlanThreads) {
     const int p = p0 + tid;
     const int used = p < mine.end && w.count[p] > 0;
@@ -367,29 +396,28 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads,
     }
     before += total;
   }
-  cluster_barrier();
+  phase_end<C>();
   const int moves = live - low;
   for (int p = gid; p < num_blocks; p += kAll) {
-    const int n = __ldcg(w.count + p);
-    moved[p] = n > 0 && p < live ? p : -1;
+    const int n = get<C>(w.count + p);
+    w.owner[p] = moved[p] = n > 0 && p < live ? p : -1;
     refs_out[p] = p < live ? n : 0;  // holes are filled below
   }
-  cluster_barrier();
+  phase_end<C>();
   for (int k = gid; k < moves; k += kAll) {
-    const int a = __ldcg(w.from + k), z = __ldcg(w.to + k);
-    moved[a] = z;
-    refs_out[z] = __ldcg(w.count + a);
+    const int a = get<C>(w.from + k), z = get<C>(w.to + k);
+    w.owner[a] = moved[a] = z;
+    refs_out[z] = get<C>(w.count + a);
     w.rows[k] = R;
   }
-  cluster_barrier();
+  phase_end<C>();
   for (long long e = gid; e < entries; e += kAll) {
     const int b = (int)(e / max_blocks), i = (int)(e % max_blocks);
-    table_out[e] = i < pages_of(len[b], R) ? __ldcg(moved + __ldcg(w.table + e)) : -1;
+    table_out[e] = i < pages_of(len[b], R) ? get<C>(w.owner + get<C>(w.table + e)) : -1;
   }
   if (gid == 0) {
     info[0] = live;
-    info[1] = moves;
-    w.head[1] = moves;
+    info[1] = w.out[0] = moves;
   }
 }
 
@@ -403,7 +431,8 @@ constexpr int kCopyThreads = 256;
 template <int N>
 __global__ void __launch_bounds__(kCopyThreads) copy_pages(const __grid_constant__ Pools<N> pools,
                                                            int R, Work w) {
-  const int n = __ldcg(w.head + 1);
+  cudaGridDependencySynchronize();  // the plan's list
+  const int n = __ldcg(w.out);
   const long long items = (long long)n * pools.items;
   for (long long it = blockIdx.x; it < items; it += gridDim.x) {
     const int k = (int)(it / pools.items);
@@ -436,7 +465,9 @@ __global__ void __launch_bounds__(kCopyThreads) copy_pages(const __grid_constant
   }
 }
 
-cudaError_t launch_copies(PoolList& pools, int R, const Work& w, cudaStream_t stream) {
+// `most`: the largest number of copies the plan can ask for.
+cudaError_t launch_copies(PoolList& pools, int R, const Work& w, long long most,
+                          cudaStream_t stream) {
   pools.items = 0;
   for (int j = 0; j < pools.n; ++j) {
     PoolDesc& d = pools.p[j];
@@ -445,18 +476,31 @@ cudaError_t launch_copies(PoolList& pools, int R, const Work& w, cudaStream_t st
     d.items = d.outer * d.chunks;
     pools.items += d.items;
   }
-  if (pools.items == 0) return cudaSuccess;
+  if (pools.items == 0 || most == 0) return cudaSuccess;
+  const int grid = most >= 148 * 6 || most * pools.items >= 148 * 6 ? 148 * 6
+                                                                   : (int)(most * pools.items);
   // The list travels with the launch, at a cost by its size: two sizes of it.
   if (pools.n <= 16) {
     Pools<16> few;
     few.items = pools.items;
     few.n = pools.n;
     for (int j = 0; j < pools.n; ++j) few.p[j] = pools.p[j];
-    copy_pages<16><<<148 * 6, kCopyThreads, 0, stream>>>(few, R, w);
-  } else {
-    copy_pages<kMaxPools><<<148 * 6, kCopyThreads, 0, stream>>>(pools, R, w);
+    return launch_early(copy_pages<16>, dim3(grid), kCopyThreads, stream, few, R, w);
   }
-  return cudaGetLastError();
+  return launch_early(copy_pages<kMaxPools>, dim3(grid), kCopyThreads, stream, pools, R, w);
+}
+
+// Shared memory of a CTA that plans alone, or 0 where the state is too large.
+template <typename K>
+cudaError_t alone_bytes(K kern, int B, int max_blocks, int num_blocks, size_t& bytes) {
+  const size_t ints = plan_ints(B, max_blocks, num_blocks);
+  bytes = 0;
+  if (ints > kAloneInts) return cudaSuccess;
+  bytes = ints * sizeof(int);
+  return bytes <= 48 << 10
+             ? cudaSuccess
+             : cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    (int)(kAloneInts * sizeof(int)));
 }
 
 }  // namespace pages
@@ -470,24 +514,34 @@ cudaError_t launch_pages_remap(const int* src, const int* old_len, const int* ne
                                int* refs_out, int* info, int B, int max_blocks, int num_blocks,
                                int block_rows, PoolList& pools, void* workspace,
                                cudaStream_t stream) {
-  const pages::Work w = pages::carve(workspace, B, max_blocks, num_blocks);
-  pages::remap_plan<<<pages::kCluster, pages::kPlanThreads, 0, stream>>>(
+  using namespace pages;
+  const Work w = carve(workspace, B, max_blocks, num_blocks);
+  size_t alone;
+  cudaError_t e = alone_bytes(remap_plan<1>, B, max_blocks, num_blocks, alone);
+  if (e != cudaSuccess) return e;
+  auto plan = alone ? remap_plan<1> : remap_plan<8>;
+  plan<<<alone ? 1 : 8, kPlanThreads, alone, stream>>>(
       src, old_len, new_len, table_in, table_out, refs_in, refs_out, info, B, max_blocks,
       num_blocks, block_rows, w);
-  cudaError_t e = cudaGetLastError();
-  return e == cudaSuccess ? pages::launch_copies(pools, block_rows, w, stream) : e;
+  e = cudaGetLastError();
+  return e == cudaSuccess ? launch_copies(pools, block_rows, w, B, stream) : e;
 }
 
 cudaError_t launch_pages_compact(const int* len, const int* table_in, int* table_out,
                                  const int* refs_in, int* refs_out, int* moved, int* info, int B,
                                  int max_blocks, int num_blocks, int block_rows, PoolList& pools,
                                  void* workspace, cudaStream_t stream) {
-  const pages::Work w = pages::carve(workspace, B, max_blocks, num_blocks);
-  pages::compact_plan<<<pages::kCluster, pages::kPlanThreads, 0, stream>>>(
+  using namespace pages;
+  const Work w = carve(workspace, B, max_blocks, num_blocks);
+  size_t alone;
+  cudaError_t e = alone_bytes(compact_plan<1>, B, max_blocks, num_blocks, alone);
+  if (e != cudaSuccess) return e;
+  auto plan = alone ? compact_plan<1> : compact_plan<8>;
+  plan<<<alone ? 1 : 8, kPlanThreads, alone, stream>>>(
       len, table_in, table_out, refs_in, refs_out, moved, info, B, max_blocks, num_blocks,
       block_rows, w);
-  cudaError_t e = cudaGetLastError();
-  return e == cudaSuccess ? pages::launch_copies(pools, block_rows, w, stream) : e;
+  e = cudaGetLastError();
+  return e == cudaSuccess ? launch_copies(pools, block_rows, w, num_blocks / 2, stream) : e;
 }
 
 }  // namespace dca
