@@ -573,8 +573,9 @@ def _call(name: str, dev: torch.device, *args) -> None:
 
 
 def _same_device(dev: torch.device, *tensors) -> None:
+    index = dev.index
     for t in tensors:
-        if t.device != dev:
+        if t.get_device() != index:
             raise DcaError(1, f"tensors on {dev} and {t.device}")
 
 

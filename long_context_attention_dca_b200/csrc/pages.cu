@@ -91,7 +91,7 @@ struct Work {  // all int32
   int* owner;   // [num_blocks] slot that keeps a partial page; a page's new index
   int* list;    // [num_blocks] free pages or holes, ascending
   int* table;   // [B * max_blocks] the table as it came
-  int* slots;   // [3][B] full pages kept, rows of the partial one, first new page
+  int* slots;   // [6][B] see Slot
 };
 constexpr int kHead = 64;
 
@@ -99,7 +99,7 @@ size_t list_ints(int B, int num_blocks) {
   return kHead + 3 * (size_t)(num_blocks > B ? num_blocks : B);
 }
 __host__ __device__ inline size_t plan_ints(int B, int max_blocks, int num_blocks) {
-  return kHead + 3 * (size_t)num_blocks + (size_t)B * max_blocks + 3 * (size_t)B;
+  return kHead + 3 * (size_t)num_blocks + (size_t)B * max_blocks + 6 * (size_t)B;
 }
 size_t work_ints(int B, int max_blocks, int num_blocks) {
   return list_ints(B, num_blocks) + plan_ints(B, max_blocks, num_blocks);
@@ -128,10 +128,35 @@ Work carve(void* ws, int B, int max_blocks, int num_blocks) {
   return w;
 }
 
-// New slot b holds the first keep = min(old_len[src[b]], new_len[b]) rows of old
-// slot src[b] (none for -1) and pages for new_len[b] rows.  Full pages are
-// shared.  A partial last page goes to the lowest slot that wants it unless it
-// is still held elsewhere; every other slot gets a copy of its rows.
+// What becomes of a slot: keep = min(old_len[src], new_len) rows of old slot src
+// (none for -1), in whole pages and rows of a partial one.  Worked out once, by
+// a thread each, so that the phases find everything beside the table.
+struct Slot {
+  int src, full, rest;
+  int pages;  // of the new length
+  int used;   // of the old length
+};  // and, sixth, where its new pages start in the list
+template <int C>
+__device__ __forceinline__ Slot slot_at(const Work& w, int B, int b) {
+  Slot s;
+  s.src = get<C>(w.slots + b);
+  s.full = get<C>(w.slots + B + b);
+  s.rest = get<C>(w.slots + 2 * (size_t)B + b);
+  s.pages = get<C>(w.slots + 3 * (size_t)B + b);
+  s.used = get<C>(w.slots + 4 * (size_t)B + b);
+  return s;
+}
+// The table as it came into the working copy: independent loads, several in
+// flight a thread, since nothing else hides their latency.
+__device__ __forceinline__ void stage(const int* from, int* to, long long n, long long first,
+                                      int step) {
+#pragma unroll 8
+  for (long long e = first; e < n; e += step) to[e] = from[e];
+}
+
+// Full pages are shared.  A partial last page goes to the lowest slot that wants
+// it unless it is still held elsewhere; every other slot gets a copy of its rows.
+// A warp walks a slot's entries.
 template <int C>
 __global__ void __cluster_dims__(C, 1, 1) __launch_bounds__(kPlanThreads, 1) remap_plan(
     const int* __restrict__ src, const int* __restrict__ old_len,
@@ -140,77 +165,82 @@ __global__ void __cluster_dims__(C, 1, 1) __launch_bounds__(kPlanThreads, 1) rem
     Work w) {
   __shared__ int sums[32];
   __shared__ int carry;
-  const int rank = blockIdx.x, tid = threadIdx.x;
-  const int gid = rank * kPlanThreads + tid;
-  constexpr int kAll = C * kPlanThreads;
+  const int rank = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
+  const int gid = rank * kPlanThreads + tid, gwarp = gid >> 5;
+  constexpr int kAll = C * kPlanThreads, kWarps = kAll / 32;
   extern __shared__ int plan_smem[];
   if (C == 1) carve_plan(w, plan_smem, B, max_blocks, num_blocks);
   cudaTriggerProgrammaticLaunchCompletion();  // the copies may take their places
-  const long long entries = (long long)B * max_blocks;
   const long long cap = (long long)max_blocks * R;
   if (rank == 0 && tid < kHead) w.head[tid] = 0;
-  for (int p = gid; p < num_blocks; p += kAll) {
-    w.count[p] = refs_in[p];
-    w.owner[p] = kNone;
-  }
-  for (long long e = gid; e < entries; e += kAll) w.table[e] = table_in[e];
-  phase_end<C>();
-
-  // drop what the slots hold; a fault anywhere refuses the whole call
   bool bad = false;
   for (int b = gid; b < B; b += kAll) {
     const int f = src[b], n = new_len[b], o = old_len[b];
-    const bool ok = f >= -1 && f < B && n >= 0 && n <= cap && o >= 0 && o <= cap;
-    bad |= !ok;
-    int keep = 0;
-    if (ok && f >= 0) keep = max(0, min(old_len[f], n));
-    w.slots[b] = keep / R;
-    w.slots[B + b] = keep % R;
+    const bool fits = o >= 0 && o <= cap;
+    bad |= f < -1 || f >= B || n < 0 || n > cap || !fits;
+    const int keep = f < 0 || f >= B ? 0 : max(0, min(old_len[f], n));
+    w.slots[b] = f;
+    w.slots[B + b] = keep / R;
+    w.slots[2 * (size_t)B + b] = keep % R;
+    w.slots[3 * (size_t)B + b] = pages_of(max(n, 0), R);
+    w.slots[4 * (size_t)B + b] = fits ? pages_of(o, R) : 0;
   }
-  for (long long e = gid; e < entries; e += kAll) {
-    const int b = (int)(e / max_blocks), i = (int)(e % max_blocks);
-    const int o = old_len[b];
-    if (o < 0 || o > cap || i >= pages_of(o, R)) continue;
-    const int p = w.table[e];
-    if (p < 0 || p >= num_blocks) bad = true;
-    else if (atomicSub(w.count + p, 1) <= 0) bad = true;  // fewer references than entries
+  stage(table_in, w.table, (long long)B * max_blocks, gid, kAll);
+#pragma unroll 4
+  for (int p = gid; p < num_blocks; p += kAll) {
+    const int n = refs_in[p];
+    w.count[p] = n;
+    w.owner[p] = kNone;
+    bad |= n < 0;
   }
-  for (int p = gid; p < num_blocks; p += kAll) bad |= refs_in[p] < 0;
+  phase_end<C>();
+
+  // what the slots hold dropped from the counts; a fault anywhere refuses the
+  // whole call
+  for (int b = gwarp; b < B; b += kWarps) {
+    const int used = get<C>(w.slots + 4 * (size_t)B + b);
+    const int* row = w.table + (size_t)b * max_blocks;
+    for (int i = lane; i < used; i += 32) {
+      const int p = get<C>(row + i);
+      if (p < 0 || p >= num_blocks) bad = true;
+      else if (atomicSub(w.count + p, 1) <= 0) bad = true;  // fewer than name it
+    }
+  }
   if (bad) atomicExch(w.head, 1);
   phase_end<C>();
   const bool fault = get<C>(w.head) != 0;
 
   // full pages are shared by every slot that keeps them
   if (!fault) {
-    for (long long e = gid; e < entries; e += kAll) {
-      const int b = (int)(e / max_blocks), i = (int)(e % max_blocks);
-      if (i < get<C>(w.slots + b)) {
-        const int f = src[b];
-        atomicAdd(w.count + get<C>(w.table + (size_t)f * max_blocks + i), 1);
-      }
+    for (int b = gwarp; b < B; b += kWarps) {
+      const Slot s = slot_at<C>(w, B, b);
+      const int* row = w.table + (size_t)max(s.src, 0) * max_blocks;
+      for (int i = lane; i < s.full; i += 32) atomicAdd(w.count + get<C>(row + i), 1);
     }
   }
   phase_end<C>();
   // partial pages that nobody holds any more go to the lowest slot
   if (!fault) {
     for (int b = gid; b < B; b += kAll) {
-      if (get<C>(w.slots + B + b) == 0) continue;
-      const int p = get<C>(w.table + (size_t)src[b] * max_blocks + get<C>(w.slots + b));
+      const Slot s = slot_at<C>(w, B, b);
+      if (s.rest == 0) continue;
+      const int p = get<C>(w.table + (size_t)s.src * max_blocks + s.full);
       if (get<C>(w.count + p) == 0) atomicMin(w.owner + p, b);
     }
   }
   phase_end<C>();
 
-  // free pages in ascending order, each CTA ranking its own part
+  // free pages, each CTA counting its own part
   const Part mine = part_of<C>(num_blocks, rank);
-  int local = 0;
-  for (int p = mine.begin + tid; p < mine.end; p += kPlanThreads)
-    local += get<C>(w.count + p) == 0 && get<C>(w.owner + p) == kNone;
-  int part_free;
-  block_scan(local, sums, part_free);
-  if (tid == 0) w.head[8 + rank] = part_free;
-  // new pages of the slots, in order; every CTA needs only the total and rank
-  // 0 writes where each slot starts
+  if (C > 1) {
+    int local = 0;
+    for (int p = mine.begin + tid; p < mine.end; p += kPlanThreads)
+      local += get<C>(w.count + p) == 0 && get<C>(w.owner + p) == kNone;
+    int part_free;
+    block_scan(local, sums, part_free);
+    if (tid == 0) w.head[8 + rank] = part_free;
+  }
+  // where each slot's new pages start among all new pages
   if (rank == 0) {
     if (tid == 0) carry = 0;
     __syncthreads();
@@ -218,92 +248,87 @@ __global__ void __cluster_dims__(C, 1, 1) __launch_bounds__(kPlanThreads, 1) rem
       const int b = b0 + tid;
       int need = 0;
       if (b < B && !fault) {
-        const int full = get<C>(w.slots + b), rest = get<C>(w.slots + B + b);
-        bool stays = false;
-        if (rest) {
-          const int p = get<C>(w.table + (size_t)src[b] * max_blocks + full);
+        const Slot s = slot_at<C>(w, B, b);
+        int stays = 0;
+        if (s.rest) {
+          const int p = get<C>(w.table + (size_t)s.src * max_blocks + s.full);
           stays = get<C>(w.owner + p) == b;
         }
-        need = pages_of(new_len[b], R) - full - (stays ? 1 : 0);
+        need = s.pages - s.full - stays;
       }
       int total;
       const int before = block_scan(need, sums, total);
-      if (b < B) w.slots[2 * B + b] = carry + before;
+      if (b < B) w.slots[5 * (size_t)B + b] = carry + before;
       __syncthreads();
-      if (tid == 0) carry = (int)min((long long)carry + total, (long long)kNone);
+      if (tid == 0) carry += total;
       __syncthreads();
     }
     if (tid == 0) w.head[2] = carry;
   }
   phase_end<C>();
 
-  int before = 0, free_all = 0;
-  for (int r = 0; r < C; ++r) {
-    const int n = get<C>(w.head + 8 + r);
-    if (r < rank) before += n;
-    free_all += n;
-  }
+  // free pages in ascending order, and the new counts
   const int need_all = get<C>(w.head + 2);
+  int before = 0, free_all = 0;
+  if (C > 1) {
+    for (int r = 0; r < C; ++r) {
+      const int n = get<C>(w.head + 8 + r);
+      if (r < rank) before += n;
+      free_all += n;
+    }
+  }
+  if (!fault && (C == 1 || need_all <= free_all)) {
+    for (int p0 = mine.begin; p0 < mine.end; p0 += kPlanThreads) {
+      const int p = p0 + tid;
+      int n = 0, free = 0;
+      if (p < mine.end) {
+        n = get<C>(w.count + p);
+        if (get<C>(w.owner + p) != kNone) n = 1;  // kept by one slot
+        free = n == 0;
+      }
+      int total;
+      const int at = before + block_scan(free, sums, total);
+      if (p < mine.end) {
+        if (free) {
+          w.list[at] = p;
+          n = at < need_all;
+        }
+        w.count[p] = n;
+      }
+      before += total;
+    }
+  }
+  if (C == 1) free_all = before;
   if (fault || need_all > free_all) {  // refused: the state as it came
-    for (long long e = gid; e < entries; e += kAll) table_out[e] = get<C>(w.table + e);
+    for (long long e = gid; e < (long long)B * max_blocks; e += kAll)
+      table_out[e] = get<C>(w.table + e);
     if (refs_out != refs_in)
       for (int p = gid; p < num_blocks; p += kAll) refs_out[p] = refs_in[p];
     if (gid == 0) {
       info[0] = fault ? kNone : -(need_all - free_all);
-      info[1] = 0;
-      w.out[0] = 0;
+      info[1] = w.out[0] = 0;
       if (fault) report_error(kDevBadArg, 209);
     }
     return;
   }
-  for (int p0 = mine.begin; p0 < mine.end; p0 += kPlanThreads) {
-    const int p = p0 + tid;
-    int n = 0, free = 0;
-    if (p < mine.end) {
-      n = get<C>(w.count + p);
-      const bool kept = get<C>(w.owner + p) != kNone;
-      if (kept) n = 1;
-      free = n == 0;
-    }
-    int total;
-    const int at = before + block_scan(free, sums, total);
-    if (p < mine.end) {
-      if (free) {
-        w.list[at] = p;
-        n = at < need_all;
-      }
-      refs_out[p] = n;
-    }
-    before += total;
-  }
   phase_end<C>();
 
-  for (long long e = gid; e < entries; e += kAll) {
-    const int b = (int)(e / max_blocks), i = (int)(e % max_blocks);
-    const int full = get<C>(w.slots + b), rest = get<C>(w.slots + B + b);
-    const int n = pages_of(new_len[b], R);
-    int page = -1;
-    if (i < n) {
-      const int* row = w.table + (size_t)max(src[b], 0) * max_blocks;
-      if (i < full) {
-        page = get<C>(row + i);
-      } else {
-        const int tail = rest ? get<C>(row + full) : -1;
-        const bool stays = rest && get<C>(w.owner + tail) == b;
-        if (i == full && stays) {
-          page = tail;
-        } else {
-          page = get<C>(w.list + get<C>(w.slots + 2 * B + b) + i - full - (stays ? 1 : 0));
-          if (i == full && rest) {
-            const int k = atomicAdd(w.head + 1, 1);
-            w.from[k] = tail;
-            w.to[k] = page;
-            w.rows[k] = rest;
-          }
-        }
-      }
+  for (int p = gid; p < num_blocks; p += kAll) refs_out[p] = get<C>(w.count + p);
+  for (int b = gwarp; b < B; b += kWarps) {
+    const Slot s = slot_at<C>(w, B, b);
+    const int* row = w.table + (size_t)max(s.src, 0) * max_blocks;
+    const int tail = s.rest ? get<C>(row + s.full) : -1;
+    const int stays = s.rest && get<C>(w.owner + tail) == b;
+    const int* fresh = w.list + get<C>(w.slots + 5 * (size_t)B + b) - s.full - stays;
+    int* out = table_out + (size_t)b * max_blocks;
+    for (int i = lane; i < max_blocks; i += 32)
+      out[i] = i >= s.pages ? -1 : i < s.full + stays ? get<C>(row + i) : get<C>(fresh + i);
+    if (lane == 0 && s.rest && !stays) {
+      const int k = atomicAdd(w.head + 1, 1);
+      w.from[k] = tail;
+      w.to[k] = get<C>(fresh + s.full);
+      w.rows[k] = s.rest;
     }
-    table_out[e] = page;
   }
   phase_end<C>();
   if (gid == 0) {
@@ -320,18 +345,25 @@ __global__ void __cluster_dims__(C, 1, 1) __launch_bounds__(kPlanThreads, 1) com
     int* refs_out, int* __restrict__ moved, int* __restrict__ info, int B, int max_blocks,
     int num_blocks, int R, Work w) {
   __shared__ int sums[32];
-  const int rank = blockIdx.x, tid = threadIdx.x;
-  const int gid = rank * kPlanThreads + tid;
-  constexpr int kAll = C * kPlanThreads;
+  const int rank = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
+  const int gid = rank * kPlanThreads + tid, gwarp = gid >> 5;
+  constexpr int kAll = C * kPlanThreads, kWarps = kAll / 32;
   extern __shared__ int plan_smem[];
   if (C == 1) carve_plan(w, plan_smem, B, max_blocks, num_blocks);
   cudaTriggerProgrammaticLaunchCompletion();  // the copies may take their places
-  const long long entries = (long long)B * max_blocks;
   const long long cap = (long long)max_blocks * R;
   const Part mine = part_of<C>(num_blocks, rank);
   if (rank == 0 && tid < 8) w.head[tid] = 0;
   bool bad = false;
   int local = 0;
+  for (int b = gid; b < B; b += kAll) {
+    const int n = len[b];
+    const bool fits = n >= 0 && n <= cap;
+    bad |= !fits;
+    w.slots[b] = fits ? pages_of(n, R) : 0;
+  }
+  stage(table_in, w.table, (long long)B * max_blocks, gid, kAll);
+#pragma unroll 4
   for (int p = mine.begin + tid; p < mine.end; p += kPlanThreads) {
     const int n = refs_in[p];
     w.count[p] = n;
@@ -341,21 +373,15 @@ __global__ void __cluster_dims__(C, 1, 1) __launch_bounds__(kPlanThreads, 1) com
   int part_live;
   block_scan(local, sums, part_live);
   if (tid == 0) w.head[8 + rank] = part_live;
-  for (long long e = gid; e < entries; e += kAll) {
-    const int b = (int)(e / max_blocks), i = (int)(e % max_blocks);
-    const int n = len[b];
-    w.table[e] = table_in[e];
-    if (n < 0 || n > cap) {
-      bad = true;
-    } else if (i < pages_of(n, R)) {
-      const int p = table_in[e];
-      // (one CTA has all counts by now, past the scan's barriers)
-      if (p < 0 || p >= num_blocks || (C == 1 ? w.count[p] : refs_in[p]) <= 0) bad = true;
+  phase_end<C>();
+  for (int b = gwarp; b < B; b += kWarps) {
+    const int used = get<C>(w.slots + b);
+    const int* row = w.table + (size_t)b * max_blocks;
+    for (int i = lane; i < used; i += 32) {
+      const int p = get<C>(row + i);
+      if (p < 0 || p >= num_blocks || get<C>(w.count + p) <= 0) bad = true;
     }
   }
-  if (max_blocks > 0)
-    for (int b = gid; b < B; b += kAll) bad |= len[b] < 0 || len[b] > cap;
-  phase_end<C>();
   if (bad) atomicExch(w.head, 1);
   int before = 0, live = 0;
   for (int r = 0; r < C; ++r) {
@@ -372,7 +398,7 @@ __global__ void __cluster_dims__(C, 1, 1) __launch_bounds__(kPlanThreads, 1) com
   if (tid == 0) w.head[16 + rank] = part_low;
   phase_end<C>();
   if (get<C>(w.head)) {
-    for (long long e = gid; e < entries; e += kAll) table_out[e] = get<C>(w.table + e);
+    for (long long e = gid; e < (long long)B * max_blocks; e += kAll) table_out[e] = get<C>(w.table + e);
     if (refs_out != refs_in)
       for (int p = gid; p < num_blocks; p += kAll) refs_out[p] = refs_in[p];
     for (int p = gid; p < num_blocks; p += kAll) moved[p] = p;
@@ -411,9 +437,11 @@ __global__ void __cluster_dims__(C, 1, 1) __launch_bounds__(kPlanThreads, 1) com
     w.rows[k] = R;
   }
   phase_end<C>();
-  for (long long e = gid; e < entries; e += kAll) {
-    const int b = (int)(e / max_blocks), i = (int)(e % max_blocks);
-    table_out[e] = i < pages_of(len[b], R) ? get<C>(w.owner + get<C>(w.table + e)) : -1;
+  for (int b = gwarp; b < B; b += kWarps) {
+    const int used = get<C>(w.slots + b);
+    const size_t row = (size_t)b * max_blocks;
+    for (int i = lane; i < max_blocks; i += 32)
+      table_out[row + i] = i < used ? get<C>(w.owner + get<C>(w.table + row + i)) : -1;
   }
   if (gid == 0) {
     info[0] = live;
