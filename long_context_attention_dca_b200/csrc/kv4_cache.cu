@@ -380,50 +380,73 @@ __device__ __forceinline__ void dequantise8(uint32_t w, uint32_t param, uint32_t
 // packed rows [T][Hkv][D], or with out_rows > 0 to row `index` of entry b of
 // [B][out_rows][Hkv][D].  code * scale + offset is formed in fp32, where it is
 // exact unless the offset is over 2^11 steps away, and rounded once.
+// One block a (run of rows, kv head), so that it reads whole tiles; a thread
+// takes kReadRows rows of the run, all their loads in flight at once.
+constexpr int kReadRows = 2;
+
 template <int D>
 __global__ void __launch_bounds__(kThreads) read_kernel(
     __nv_bfloat16* __restrict__ Ko, __nv_bfloat16* __restrict__ Vo, Pages pg,
     const int* __restrict__ cu, const int* __restrict__ t0, int B, int T, int out_rows) {
   using TL = Tile<D>;
-  constexpr int kLanes = D / 16;
+  constexpr int kLanes = D / 16, kRows = kThreads / kLanes;
   const long long cap = out_rows > 0
                             ? min((long long)pg.max_blocks * pg.block_rows, (long long)out_rows)
                             : (long long)pg.max_blocks * pg.block_rows;
   if (blockIdx.x == gridDim.x - 1) {
-    check_offsets(T, cu, t0, B, cap);
+    if (blockIdx.y == 0) check_offsets(T, cu, t0, B, cap);
     return;
   }
-  const long long gid = (long long)blockIdx.x * (kThreads / kLanes) + threadIdx.x / kLanes;
-  const int i = threadIdx.x % kLanes;
-  if (gid >= (long long)T * pg.Hkv) return;
-  // heads outermost inside a run of rows, so that a block reads whole tiles
-  const int run = 64;
-  const long long per = (long long)run * pg.Hkv;
-  const int r0 = (int)(gid / per) * run, n = min(run, T - r0);
-  const int h = (int)((gid % per) / n), row = r0 + (int)((gid % per) % n);
-  const RowAt at = locate(row, T, cu, t0, B, cap);
-  if (at.b < 0) return;
-  const uint8_t* tile = tile_of<D>(pg, at.b, at.pos, h);
-  if (tile == nullptr) {
-    if (i == 0 && h == 0) report_error(kDevBadArg, 206);
-    return;
-  }
-  const int r = at.pos % kTileKeys;
-  const long long orow = out_rows > 0 ? (long long)at.b * out_rows + at.pos : row;
-  const size_t dst = ((size_t)orow * pg.Hkv + h) * D + 8 * i;
+  const int i = threadIdx.x % kLanes, h = blockIdx.y;
+  size_t dst[kReadRows];
+  uint32_t w[kReadRows][2][4];
+  bool live[kReadRows];
 #pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    const int g = D == 128 ? half : 0, word = D == 128 ? i : i + 4 * half;
-    const uint32_t wk = __ldg(reinterpret_cast<const uint32_t*>(tile + TL::k_word(r, g, word)));
-    const uint32_t wv = __ldg(reinterpret_cast<const uint32_t*>(tile + TL::v_word(r, g, word)));
-    const uint32_t pk = __ldg(reinterpret_cast<const uint32_t*>(tile + TL::k_param(r, g)));
-    const uint32_t pv = __ldg(reinterpret_cast<const uint32_t*>(tile + TL::v_param(r, g)));
-    uint32_t k[4], v[4];
-    dequantise8(wk, pk, k);
-    dequantise8(wv, pv, v);
-    *reinterpret_cast<uint4*>(Ko + dst + half * (D / 2)) = make_uint4(k[0], k[1], k[2], k[3]);
-    *reinterpret_cast<uint4*>(Vo + dst + half * (D / 2)) = make_uint4(v[0], v[1], v[2], v[3]);
+  for (int n = 0; n < kReadRows; ++n) {
+    const int row = (blockIdx.x * kReadRows + n) * kRows + threadIdx.x / kLanes;
+    live[n] = false;
+    if (row >= T) continue;
+    const RowAt at = locate(row, T, cu, t0, B, cap);
+    if (at.b < 0) continue;
+    const uint8_t* tile = tile_of<D>(pg, at.b, at.pos, h);
+    if (tile == nullptr) {
+      if (i == 0 && h == 0) report_error(kDevBadArg, 206);
+      continue;
+    }
+    const int r = at.pos % kTileKeys;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int g = D == 128 ? half : 0, word = D == 128 ? i : i + 4 * half;
+      w[n][half][0] = __ldg(reinterpret_cast<const uint32_t*>(tile + TL::k_word(r, g, word)));
+      w[n][half][1] = __ldg(reinterpret_cast<const uint32_t*>(tile + TL::v_word(r, g, word)));
+      w[n][half][2] = __ldg(reinterpret_cast<const uint32_t*>(tile + TL::k_param(r, g)));
+      w[n][half][3] = __ldg(reinterpret_cast<const uint32_t*>(tile + TL::v_param(r, g)));
+    }
+    const long long orow = out_rows > 0 ? (long long)at.b * out_rows + at.pos : row;
+    dst[n] = ((size_t)orow * pg.Hkv + h) * D + 8 * i;
+    live[n] = true;
   }
+#pragma unroll
+  for (int n = 0; n < kReadRows; ++n) {
+    if (!live[n]) continue;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      uint32_t k[4], v[4];
+      dequantise8(w[n][half][0], w[n][half][2], k);
+      dequantise8(w[n][half][1], w[n][half][3], v);
+      const size_t to = dst[n] + half * (D / 2);
+      *reinterpret_cast<uint4*>(Ko + to) = make_uint4(k[0], k[1], k[2], k[3]);
+      *reinterpret_cast<uint4*>(Vo + to) = make_uint4(v[0], v[1], v[2], v[3]);
+    }
+  }
+}
+
+// Heads of a block: what a thread works out for its row serves them all, so as
+// many as leave 4 blocks an SM.
+inline int heads_per_block(long long row_blocks, int Hkv) {
+  int n = Hkv;
+  while (n > 1 && row_blocks * ((Hkv + n - 1) / n) < 148 * 4) n = (n + 1) / 2;
+  return n;
 }
 
 template <int D>
@@ -431,10 +454,7 @@ cudaError_t launch_append_t(const void* k_new, const void* v_new, const Pages& p
                             const int* t0, int B, int T, int s, float base, cudaStream_t stream) {
   constexpr int kRows = kThreads / (D / 16);
   const unsigned gx = (unsigned)((T + kRows - 1) / kRows);
-  // The angles of a row serve all heads of a block, so a block takes as many
-  // heads as leave 4 blocks an SM.
-  int hpc = pg.Hkv;
-  while (hpc > 1 && (long long)gx * ((pg.Hkv + hpc - 1) / hpc) < 148 * 4) hpc = (hpc + 1) / 2;
+  const int hpc = heads_per_block(gx, pg.Hkv);
   const unsigned gy = (unsigned)((pg.Hkv + hpc - 1) / hpc);
   append_kernel<D><<<dim3(gx + 1, gy), kThreads, 0, stream>>>(
       static_cast<const __nv_bfloat16*>(k_new), static_cast<const __nv_bfloat16*>(v_new), pg, cu,
@@ -446,10 +466,9 @@ template <int D>
 cudaError_t launch_read_t(void* K, void* V, const Pages& pg, const int* cu, const int* t0, int B,
                           int T, int out_rows, cudaStream_t stream) {
   constexpr int kRows = kThreads / (D / 16);
-  const unsigned grid = (unsigned)(((long long)T * pg.Hkv + kRows - 1) / kRows);
-  read_kernel<D><<<grid + 1, kThreads, 0, stream>>>(static_cast<__nv_bfloat16*>(K),
-                                                static_cast<__nv_bfloat16*>(V), pg, cu, t0, B, T,
-                                                out_rows);
+  const unsigned gx = (unsigned)(((long long)T + kRows * kReadRows - 1) / (kRows * kReadRows));
+  read_kernel<D><<<dim3(gx + 1, pg.Hkv), kThreads, 0, stream>>>(
+      static_cast<__nv_bfloat16*>(K), static_cast<__nv_bfloat16*>(V), pg, cu, t0, B, T, out_rows);
   return cudaGetLastError();
 }
 
