@@ -22,7 +22,7 @@
 namespace dca {
 namespace kv4 {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 
 // A double rounded once to bf16 (nearest even): to fp32 toward zero with the
 // lost bits kept as a sticky last bit, which the second rounding cannot confuse
@@ -38,12 +38,6 @@ __device__ __forceinline__ uint32_t bf16_bits_of(double x) {
 __device__ __forceinline__ void split16(double x, float& hi, float& lo) {
   hi = __uint_as_float(__float_as_uint((float)x) & 0xFFFFFF00u);
   lo = (float)(x - (double)hi);
-}
-
-// True when y may lie within `tol` of the midpoint of two bf16 values.
-__device__ __forceinline__ bool near_bf16_border(float y, float tol) {
-  const float mid = __uint_as_float((__float_as_uint(y) & 0xFFFF0000u) | 0x8000u);
-  return fabsf(y - mid) <= tol;
 }
 
 __device__ __forceinline__ __nv_bfloat162 as_bf162(uint32_t w) {
@@ -69,6 +63,17 @@ __device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
   uint64_t d;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
+}
+
+// Two results rounded to bf16, and where their errors (under 2.4e-7 of them)
+// leave that open: bits that differ between the roundings of the two ends.
+__device__ __forceinline__ uint32_t rounded(uint64_t y, uint32_t& open) {
+  float a, b, c, d;
+  f2_unpack(f2_mul(y, f2_pack(1.00000024f, 1.00000024f)), a, b);
+  f2_unpack(f2_mul(y, f2_pack(0.99999976f, 0.99999976f)), c, d);
+  const uint32_t one = pack_bf16(a, b), other = pack_bf16(c, d);
+  open = one ^ other;
+  return one;
 }
 
 struct Params {
@@ -147,16 +152,16 @@ __device__ __forceinline__ uint32_t quantise8(const uint32_t (&w)[4], const Para
     far = fmax3(far, fabsf(r0), fabsf(r1));
   }
   const float half = 0.5f * p.scale;
-  const bool tiny = p.inv == INFINITY;  // a scale whose reciprocal overflows
-  if ((far >= half && p.scale > 0.f) || tiny) {
-    bool mend = far > half || tiny;
-    const __nv_bfloat162 least =
-        __hmin2(__hmin2(as_bf162(w[0] & 0x7FFF7FFFu), as_bf162(w[1] & 0x7FFF7FFFu)),
-                __hmin2(as_bf162(w[2] & 0x7FFF7FFFu), as_bf162(w[3] & 0x7FFF7FFFu)));
-    mend |= fminf(bf16_lo(as_u32(least)), bf16_hi(as_u32(least))) <
-            fabsf(p.off) * 1.220703125e-4f;  // 2^-13 of half the offset
-    if (mend) return mend_codes(make_uint4(w[0], w[1], w[2], w[3]), p.off, p.scale);
-  }
+  // Only a value far below the offset makes d inexact, which matters on a border.
+  const __nv_bfloat162 least =
+      __hmin2(__hmin2(__habs2(as_bf162(w[0])), __habs2(as_bf162(w[1]))),
+              __hmin2(__habs2(as_bf162(w[2])), __habs2(as_bf162(w[3]))));
+  const bool small = fminf(bf16_lo(as_u32(least)), bf16_hi(as_u32(least))) <
+                     fabsf(p.off) * 1.220703125e-4f;  // 2^-13 of half the offset
+  // (no scale: a constant group or one that is not finite, codes 0; an infinite
+  // reciprocal: a subnormal scale)
+  if (half > 0.f && (far > half || (small && far == half) || p.inv == INFINITY))
+    return mend_codes(make_uint4(w[0], w[1], w[2], w[3]), p.off, p.scale);
   const float lo = fmaf(c[3], 4096.f, fmaf(c[2], 256.f, fmaf(c[1], 16.f, c[0])));
   const float hi = fmaf(c[7], 4096.f, fmaf(c[6], 256.f, fmaf(c[5], 16.f, c[4])));
   return __float2uint_rz(lo) | (__float2uint_rz(hi) << 16);
@@ -270,40 +275,38 @@ __global__ void __launch_bounds__(kThreads) append_kernel(
         const uint64_t n2 = f2_pack(bf16_lo(b[n] ^ 0x80008000u), bf16_hi(b[n] ^ 0x80008000u));
         const ulonglong2 c = turn[n][0][threadIdx.x], sn = turn[n][1][threadIdx.x];
         // products with the 16-bit parts are exact in fp32
+        uint32_t b0, b1;  // not 0 next to a border
         const uint64_t o0 = f2_add(f2_fma(p2, c.x, f2_mul(n2, sn.x)),
                                    f2_fma(p2, c.y, f2_mul(n2, sn.y)));
         const uint64_t o1 = f2_add(f2_fma(q2, c.x, f2_mul(p2, sn.x)),
                                    f2_fma(q2, c.y, f2_mul(p2, sn.y)));
-        float y0, y1, z0, z1;
-        f2_unpack(o0, y0, y1);
-        f2_unpack(o1, z0, z1);
-        const float t0 = (fabsf(bf16_lo(a[n])) + fabsf(bf16_lo(b[n]))) * 1e-11f;
-        const float t1 = (fabsf(bf16_hi(a[n])) + fabsf(bf16_hi(b[n]))) * 1e-11f;
-        if (near_bf16_border(y0, fmaf(fabsf(y0), 2.4e-7f, t0)) ||
-            near_bf16_border(z0, fmaf(fabsf(z0), 2.4e-7f, t0)))
-          again |= 1u << (2 * n);
-        if (near_bf16_border(y1, fmaf(fabsf(y1), 2.4e-7f, t1)) ||
-            near_bf16_border(z1, fmaf(fabsf(z1), 2.4e-7f, t1)))
-          again |= 2u << (2 * n);
-        k[0][n] = pack_bf16(y0, y1);
-        k[1][n] = pack_bf16(z0, z1);
+        k[0][n] = rounded(o0, b0);
+        k[1][n] = rounded(o1, b1);
+        // A result far below its operands has a larger error than its own size
+        // tells: that is a border too.
+        const __nv_bfloat162 size = __hadd2(__habs2(as_bf162(a[n])), __habs2(as_bf162(b[n])));
+        const __nv_bfloat162 much = __float2bfloat162_rn(4096.f);
+        b0 |= as_u32(__hsub2(__hmul2(__habs2(as_bf162(k[0][n])), much), size)) & 0x80008000u;
+        b1 |= as_u32(__hsub2(__hmul2(__habs2(as_bf162(k[1][n])), much), size)) & 0x80008000u;
+        if (b0 | b1) again |= 1u << n;
       }
-      while (again) {
-        const int m = __ffs(again) - 1;
+      while (again) {  // both elements of the pair once more, in fp64
+        const int n = __ffs(again) - 1;
         again &= again - 1;
-        double c, sn;
-        sincos64((double)pos * theta.v[8 * i + m], c, sn);
-        const double p = (double)__bfloat162float(k_new[src + m]);
-        const double q = (double)__bfloat162float(k_new[src + D / 2 + m]);
-        const int sh = (m & 1) * 16;
-        const uint32_t keep = ~(0xFFFFu << sh);
-        const uint32_t z0 = bf16_bits_of(fma(p, c, -(q * sn))) << sh;
-        const uint32_t z1 = bf16_bits_of(fma(q, c, p * sn)) << sh;
+        uint32_t z0 = 0, z1 = 0;
+        for (int u = 0; u < 2; ++u) {
+          double c, sn;
+          sincos64((double)pos * theta.v[8 * i + 2 * n + u], c, sn);
+          const double p = (double)__bfloat162float(k_new[src + 2 * n + u]);
+          const double q = (double)__bfloat162float(k_new[src + D / 2 + 2 * n + u]);
+          z0 |= bf16_bits_of(fma(p, c, -(q * sn))) << (16 * u);
+          z1 |= bf16_bits_of(fma(q, c, p * sn)) << (16 * u);
+        }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          if (j == m / 2) {
-            k[0][j] = (k[0][j] & keep) | z0;
-            k[1][j] = (k[1][j] & keep) | z1;
+          if (j == n) {
+            k[0][j] = z0;
+            k[1][j] = z1;
           }
         }
       }
