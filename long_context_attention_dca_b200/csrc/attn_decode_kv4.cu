@@ -53,15 +53,25 @@ constexpr int kMaxTiles = 512;  // of a CTA's share, so that their places fit in
 // piece raises one of the two, so no slot is used twice.
 constexpr int kSetup = 12;
 struct Split {
-  long long tiles;  // of all units
-  long long shares;
+  long long shares, each, extra;  // the first `extra` shares hold one tile more
 };
-__host__ __device__ inline long long share_begin(const Split& sp, long long c) {
-  return c * sp.tiles / sp.shares;
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? (unsigned)a / (unsigned)b : a / b;
+}
+__device__ __forceinline__ Split make_split(long long tiles, long long shares) {
+  Split sp;
+  sp.shares = shares;
+  sp.each = quotient(tiles, shares);
+  sp.extra = tiles - sp.each * shares;
+  return sp;
+}
+__device__ __forceinline__ long long share_begin(const Split& sp, long long c) {
+  return c * sp.each + (c < sp.extra ? c : sp.extra);
 }
 // The share that holds tile g.
 __device__ __forceinline__ long long share_of(const Split& sp, long long g) {
-  return ((g + 1) * sp.shares - 1) / sp.tiles;
+  const long long most = sp.extra * (sp.each + 1);
+  return g < most ? quotient(g, sp.each + 1) : sp.extra + quotient(g - most, sp.each);
 }
 inline int head_groups(int Hq, int Hkv) { return (Hq / Hkv + kHeads - 1) / kHeads; }
 // Shares of `tiles` tiles: one for every four (a tile a warp), at most `most`.
@@ -85,11 +95,12 @@ struct DecodeSmem {
   // [piece][hi, lo][group][head][word] x 16 bytes of query fragments
   static constexpr int kQ = 3 * 2 * (D / 64) * kHeads * 8 * 16;
   static constexpr int kCs = 3 * (D / 2) * 8;          // cos, sin
+  static constexpr int kRaw = kHeads * D * 2;          // queries as they came
   static constexpr int kSums = 3 * kHeads * (D / 64) * 4;  // sum of q per group
   static constexpr int kF = kHeads * 4;
   static constexpr int kBars = kWarps * kRing * 8 + 16;  // + abort and page words
   static constexpr int kPlaces = kMaxTiles * 4;  // pool tile of every tile of the share
-  static constexpr int kTotal = kRings + kQ + kCs + kSums + kF + kBars + kPlaces;
+  static constexpr int kTotal = kRings + kQ + kRaw + kCs + kSums + kF + kBars + kPlaces;
   static_assert(kWarps * kHeads * (D + 2) * 4 <= kRings, "merge area");
 };
 
@@ -170,12 +181,13 @@ __global__ void __launch_bounds__(kDecodeThreads, kCtasPerSm) decode_kernel(
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ long long sums[kWarps];
   uint8_t* qf = smem + SM::kRings;
-  float2* cs = reinterpret_cast<float2*>(qf + SM::kQ);
-  float* qsum = reinterpret_cast<float*>(qf + SM::kQ + SM::kCs);  // [piece][head][group]
+  __nv_bfloat16* qraw = reinterpret_cast<__nv_bfloat16*>(qf + SM::kQ);
+  float2* cs = reinterpret_cast<float2*>(qf + SM::kQ + SM::kRaw);
+  float* qsum = reinterpret_cast<float*>(qf + SM::kQ + SM::kRaw + SM::kCs);  // [piece][head][group]
   float* qexp = qsum + 3 * kHeads * kGr;                          // [head]
   uint8_t* bars = reinterpret_cast<uint8_t*>(qexp + kHeads);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + kWarps * kRing * 8);
-  volatile int* bad_page = abort_flag + 1;
+  volatile int* bad_pages = abort_flag + 1;  // [2], of this piece and of the next
   uint32_t* places = reinterpret_cast<uint32_t*>(bars + SM::kBars);
 
   cudaTriggerProgrammaticLaunchCompletion();  // the merge may take its places
@@ -184,12 +196,12 @@ __global__ void __launch_bounds__(kDecodeThreads, kCtasPerSm) decode_kernel(
   const int tpb = pg.block_rows / kTileKeys;
   const long long cap = (long long)pg.max_blocks * pg.block_rows;
   const long long all = spans_before(t, B, cap, sums) * per_seq;
-  const Split split{all, share_count(all, gridDim.x)};
+  const Split split = make_split(all, share_count(all, gridDim.x));
   if (blockIdx.x == 0) {  // positions outside the cache: reported, no work
     for (int b = tid; b < B; b += kDecodeThreads)
       if (tiles_of(__ldg(t + b), cap) == 0) report_error(kDevBadArg, 207);
   }
-  if (blockIdx.x >= split.shares || split.tiles == 0) return;
+  if (blockIdx.x >= split.shares || all == 0) return;
   long long at = share_begin(split, blockIdx.x);
   const long long end = share_begin(split, blockIdx.x + 1);
   // the sequence at the share's begin, and where that sequence begins (every
@@ -224,10 +236,16 @@ __global__ void __launch_bounds__(kDecodeThreads, kCtasPerSm) decode_kernel(
   const uint8_t* ring = smem + warp * kRing * SM::kHalf;
   const uint32_t full0 = smem_u32(bars) + warp * kRing * 8;
   int buf = 0, phase = 0;
+  if (tid == 0) bad_pages[0] = bad_pages[1] = 0;
+  for (int i = tid; i < SM::kQ / 16; i += kDecodeThreads)  // heads a unit does not have
+    reinterpret_cast<uint4*>(qf)[i] = make_uint4(0, 0, 0, 0);
+  for (int i = tid; i < 3 * kHeads * kGr + kHeads; i += kDecodeThreads) qsum[i] = 0.f;
+  int turned = -1;  // the sequence whose rotations cs holds
 
-  while (at < end) {
+  for (int piece = 0; at < end; ++piece) {
+  volatile int* bad_page = bad_pages + (piece & 1);
   const int tb = __ldg(t + b), all_tiles = tiles_of(tb, cap), span = all_tiles + kSetup;
-  const int unit = (int)((at - b_at) / span);
+  const int unit = (int)quotient(at - b_at, span);
   const long long unit_at = b_at + (long long)unit * span;
   const int tile0 = max(0, (int)(at - unit_at) - kSetup);
   const int tile1 = max(0, (int)(min(end - unit_at, (long long)span)) - kSetup);
@@ -243,8 +261,13 @@ __global__ void __launch_bounds__(kDecodeThreads, kCtasPerSm) decode_kernel(
   const int hg = unit % n_hg, hk = unit / n_hg;
   const int h_base = hk * G + hg * kHeads;
   const int n_heads = min(kHeads, G - hg * kHeads);
-  if (tid == 0) *bad_page = 0;
-  __syncthreads();
+  __syncthreads();  // the piece before is done
+  if (tid == 0) bad_pages[~piece & 1] = 0;
+  // everything the piece begins with, in flight at once: its pages, its queries
+  const bool has_q = tid < n_heads * D / 8;
+  uint4 q8 = {};
+  if (has_q)
+    q8 = __ldg(reinterpret_cast<const uint4*>(q + ((size_t)seq * Hq + h_base) * D) + tid);
   for (int i = tid; i < n_tiles; i += kDecodeThreads) {
     const int tile = tile0 + i;
     int blk = __ldg(pg.table + (size_t)seq * pg.max_blocks + tile / tpb);
@@ -254,6 +277,18 @@ __global__ void __launch_bounds__(kDecodeThreads, kCtasPerSm) decode_kernel(
       blk = 0;
     }
     places[i] = (uint32_t)(((size_t)blk * pg.Hkv + hk) * tpb + tile % tpb);
+  }
+  if (has_q) reinterpret_cast<uint4*>(qraw)[tid] = q8;
+  if (turned != seq) {
+    const int im = tb % s;
+#pragma unroll 1
+    for (int x = tid; x < 3 * (D / 2); x += kDecodeThreads) {
+      const int p = x / (D / 2), k = x % (D / 2);
+      double cd, sd;
+      sincos64((double)query_pos_for_piece(p, im, s, c) * theta.v[k], cd, sd);
+      cs[x] = make_float2((float)cd, (float)sd);
+    }
+    turned = seq;
   }
   __syncthreads();
   const int parts = n_tiles > warp ? 2 * ((n_tiles - warp + kWarps - 1) / kWarps) : 0;
@@ -271,27 +306,15 @@ __global__ void __launch_bounds__(kDecodeThreads, kCtasPerSm) decode_kernel(
 
   // ---------------- queries: three rotations, fragments, group sums ----------------
   {
-    const int im = tb % s;
-#pragma unroll 1
-    for (int x = tid; x < 3 * (D / 2); x += kWarps * 32) {
-      const int p = x / (D / 2), k = x % (D / 2);
-      double cd, sd;
-      sincos64((double)query_pos_for_piece(p, im, s, c) * theta.v[k], cd, sd);
-      cs[x] = make_float2((float)cd, (float)sd);
-    }
-    __syncthreads();
     constexpr int kPairs = D / 64;  // (k, k + D/2) pairs a lane owns of a head
 #pragma unroll 1
-    for (int hh = warp; hh < kHeads; hh += kWarps) {
+    for (int job = warp; job < 3 * n_heads; job += kWarps) {  // a head and a piece
+      const int hh = job / 3, p = job % 3;
       float x0[kPairs], x1[kPairs], big = 0.f;
 #pragma unroll
       for (int u = 0; u < kPairs; ++u) {
-        x0[u] = x1[u] = 0.f;
-        if (hh < n_heads) {
-          const __nv_bfloat16* row = q + ((size_t)seq * Hq + h_base + hh) * D + lane + 32 * u;
-          x0[u] = __bfloat162float(row[0]) * scale_log2;
-          x1[u] = __bfloat162float(row[D / 2]) * scale_log2;
-        }
+        x0[u] = __bfloat162float(qraw[hh * D + lane + 32 * u]) * scale_log2;
+        x1[u] = __bfloat162float(qraw[hh * D + lane + 32 * u + D / 2]) * scale_log2;
         big = fmaxf(big, fabsf(x0[u]) + fabsf(x1[u]));
       }
 #pragma unroll
@@ -299,8 +322,7 @@ __global__ void __launch_bounds__(kDecodeThreads, kCtasPerSm) decode_kernel(
       // every rotated value times 2^-e stays below 2^13
       const int e = big > 0.f ? (int)(__float_as_uint(big) >> 23) - 127 - 12 : 0;
       const float down = ldexpf(1.f, -(e / 2)), down2 = ldexpf(1.f, -(e - e / 2));
-#pragma unroll 1
-      for (int p = 0; p < 3; ++p) {
+      {
         float sum[2] = {0.f, 0.f};
 #pragma unroll
         for (int u = 0; u < kPairs; ++u) {
@@ -330,7 +352,7 @@ __global__ void __launch_bounds__(kDecodeThreads, kCtasPerSm) decode_kernel(
         const float unit = down * down2 * 5.9604644775390625e-8f;  // 2^-24
         if (lane < kGr) qsum[(p * kHeads + hh) * kGr + lane] = (lane == 0 ? sum[0] : sum[1]) * unit;
       }
-      if (lane == 0) qexp[hh] = ldexpf(1.f, e + 24);
+      if (lane == 0 && p == 0) qexp[hh] = ldexpf(1.f, e + 24);
     }
     __syncthreads();
   }
@@ -662,7 +684,7 @@ __global__ void __launch_bounds__(kMergeThreads) decode_merge(
     if (d == 0) LSE[row] = __int_as_float(0x7fc00000);
     return;
   }
-  const Split split{all, share_count(all, grid_shares)};
+  const Split split = make_split(all, share_count(all, grid_shares));
   const long long c0 = share_of(split, g0);
   const int n = (int)(share_of(split, g0 + tiles - 1) - c0) + 1;
   const size_t slot0 = ((size_t)b * per_seq + unit + c0) * kHeads + hh;
@@ -701,6 +723,10 @@ __global__ void __launch_bounds__(kMergeThreads) decode_merge(
   if (d == 0) LSE[row] = (mu + log2f(total)) * 0.69314718055994530942f;
 }
 
+namespace {
+std::atomic<unsigned long long> g_smem_set[2];  // by head size: a bit a device
+}
+
 template <int D>
 cudaError_t launch_decode_t(const void* q, const Pages& pg, const int* t, void* O, float* LSE,
                             int B, int Hq, int s, int c, float base, float scale,
@@ -714,7 +740,7 @@ cudaError_t launch_decode_t(const void* q, const Pages& pg, const int* t, void* 
   auto kern = decode_kernel<D>;
   constexpr int smem = DecodeSmem<D>::kTotal;
   // once a device: the attribute stays with the function there
-  static std::atomic<unsigned long long> set{0};
+  std::atomic<unsigned long long>& set = g_smem_set[D / 128];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess && (dev >= 64 || !(set.load() >> dev & 1))) {
