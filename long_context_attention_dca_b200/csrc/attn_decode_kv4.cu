@@ -30,7 +30,6 @@
 #include "dca_index.cuh"
 #include "dca_kernels.cuh"
 #include "kv4.cuh"
-#include "softmax_sm100.cuh"
 
 namespace dca {
 namespace kv4 {
@@ -359,19 +358,20 @@ __global__ void __launch_bounds__(kDecodeThreads, kCtasPerSm) decode_kernel(
 
   const int g = lane >> 2, t4 = lane & 3;
   float m_run[2] = {-INFINITY, -INFINITY};  // heads 2 t4, 2 t4 + 1
-  float l_run[2] = {0.f, 0.f};
+  float l_run[2];
+  uint64_t l2 = f2_pack(0.f, 0.f);          // sums of both heads
   float off[kGr][2];                        // sum of p * offset, by group
-  float o[kGr * 4][4];                      // times 2^-24; rows g + 8 times 16 besides
+  // pairs of heads, rows g and g + 8; times 2^-24, rows g + 8 times 16 besides
+  uint64_t o[kGr * 4][2];
 #pragma unroll
-  for (int i = 0; i < kGr * 4; ++i)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
+  for (int i = 0; i < kGr * 4; ++i) o[i][0] = o[i][1] = f2_pack(0.f, 0.f);
 #pragma unroll
   for (int i = 0; i < kGr; ++i) off[i][0] = off[i][1] = 0.f;
 
   {
     // ---------------- tiles ----------------
     const float F[2] = {qexp[2 * t4], qexp[2 * t4 + 1]};
+    const uint64_t F2 = f2_pack(F[0], F[1]);
     // first keys of the query's own chunk and of the one before
     const int own0 = tb - tb % s, prev0 = own0 - s;
     const int kr = 4 * (g >> 1) + (g & 1);  // MMA row g holds key kr, row g + 8 key kr + 2
@@ -504,29 +504,34 @@ __global__ void __launch_bounds__(kDecodeThreads, kCtasPerSm) decode_kernel(
         mx[e] *= F[e];
       }
       if (__any_sync(0xFFFFFFFFu, mx[0] > m_run[0] || mx[1] > m_run[1])) {
+        float al[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const float mn = fmaxf(m_run[e], mx[e]);
-          const float al = fast_exp2(m_run[e] - (mn == -INFINITY ? 0.f : mn));
+          al[e] = fast_exp2(m_run[e] - (mn == -INFINITY ? 0.f : mn));
           m_run[e] = mn;
-          l_run[e] *= al;
 #pragma unroll
-          for (int gr = 0; gr < kGr; ++gr) off[gr][e] *= al;
+          for (int gr = 0; gr < kGr; ++gr) off[gr][e] *= al[e];
+        }
+        const uint64_t al2 = f2_pack(al[0], al[1]);
+        l2 = f2_mul(l2, al2);
 #pragma unroll
-          for (int i = 0; i < kGr * 4; ++i) {
-            o[i][e] *= al;
-            o[i][e + 2] *= al;
-          }
+        for (int i = 0; i < kGr * 4; ++i) {
+          o[i][0] = f2_mul(o[i][0], al2);
+          o[i][1] = f2_mul(o[i][1], al2);
         }
       }
-      const float mu[2] = {m_run[0] == -INFINITY ? 0.f : m_run[0],
-                           m_run[1] == -INFINITY ? 0.f : m_run[1]};
+      const uint64_t mu2 = f2_pack(m_run[0] == -INFINITY ? 0.f : -m_run[0],
+                                   m_run[1] == -INFINITY ? 0.f : -m_run[1]);
 #pragma unroll
       for (int sub = 0; sub < 4; ++sub)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          x[sub][e] = fast_exp2(fmaf(x[sub][e], F[e & 1], -mu[e & 1]));
-          l_run[e & 1] += x[sub][e];
+        for (int e = 0; e < 4; e += 2) {
+          float p0, p1;
+          f2_unpack(f2_fma(f2_pack(x[sub][e], x[sub][e + 1]), F2, mu2), p0, p1);
+          x[sub][e] = fast_exp2(p0);
+          x[sub][e + 1] = fast_exp2(p1);
+          l2 = f2_add(l2, f2_pack(x[sub][e], x[sub][e + 1]));
         }
       if (!warp_wait(full0 + 8 * buf, phase, abort_flag, 403)) break;
       const uint8_t* tile = ring + buf * SM::kHalf - SM::kHalf;  // V offsets count from the tile
@@ -555,6 +560,7 @@ __global__ void __launch_bounds__(kDecodeThreads, kCtasPerSm) decode_kernel(
             max(__reduce_max_sync(0xFFFFFFFFu, most & 0xFFFFu) >> 7, 40u);
         const uint32_t up = (141u - ex) << 23;
         const float down = __uint_as_float((ex - 14u) << 23);
+        const uint64_t down2 = f2_pack(down, down);
         float acc[4][4];
 #pragma unroll
         for (int sub = 0; sub < 4; ++sub) {
@@ -584,10 +590,13 @@ __global__ void __launch_bounds__(kDecodeThreads, kCtasPerSm) decode_kernel(
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) o[gr * 4 + i][e] = fmaf(acc[i][e], down, o[gr * 4 + i][e]);
+          for (int u = 0; u < 2; ++u)
+            o[gr * 4 + i][u] =
+                f2_fma(f2_pack(acc[i][2 * u], acc[i][2 * u + 1]), down2, o[gr * 4 + i][u]);
       }
       next_part();
     }
+    f2_unpack(l2, l_run[0], l_run[1]);
 #pragma unroll
     for (int sh = 4; sh <= 16; sh <<= 1) {
 #pragma unroll
@@ -619,8 +628,11 @@ __global__ void __launch_bounds__(kDecodeThreads, kCtasPerSm) decode_kernel(
         for (int e = 0; e < 2; ++e) {
           // rows g and g + 8 are dims 2m and 2m + 1 of word g
           float* at = mo + (warp * kHeads + 2 * t4 + e) * D + gr * 64 + 8 * g + 2 * m;
-          at[0] = fmaf(o[gr * 4 + m][e], 16777216.f, off[gr][e]);     // 2^24
-          at[1] = fmaf(o[gr * 4 + m][e + 2], 1048576.f, off[gr][e]);  // 2^24 / 16
+          float lo[2], hi[2];
+          f2_unpack(o[gr * 4 + m][0], lo[0], lo[1]);
+          f2_unpack(o[gr * 4 + m][1], hi[0], hi[1]);
+          at[0] = fmaf(lo[e], 16777216.f, off[gr][e]);  // 2^24
+          at[1] = fmaf(hi[e], 1048576.f, off[gr][e]);   // 2^24 / 16
         }
     if (g == 0) {
 #pragma unroll

@@ -26,9 +26,16 @@
 #include <cmath>
 
 #include "dca_common.cuh"
+#include "softmax_sm100.cuh"
 
 namespace dca {
 namespace kv4 {
+
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
 
 constexpr int kTileKeys = 64;
 constexpr int kGroup = 64;

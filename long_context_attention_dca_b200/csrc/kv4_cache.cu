@@ -17,7 +17,6 @@
 #include "dca_common.cuh"
 #include "dca_kernels.cuh"
 #include "kv4.cuh"
-#include "softmax_sm100.cuh"
 
 namespace dca {
 namespace kv4 {
@@ -57,12 +56,6 @@ __device__ __forceinline__ uint32_t min_negmax(const uint32_t (&w)[4]) {
   // (a.lo, -b.lo) against (a.hi, -b.hi)
   const uint32_t lo = __byte_perm(ua, ub, 0x5410), hi = __byte_perm(ua, ub, 0x7632);
   return as_u32(__hmin2_nan(as_bf162(lo), as_bf162(hi)));
-}
-
-__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
 }
 
 // Two results rounded to bf16, and where their errors (under 2.4e-7 of them)
