@@ -169,14 +169,52 @@ __device__ __forceinline__ long long spans_before(const int* t, int n, long long
   return x;
 }
 
-template <int D>
+// O += weights * values of group gr over a 64-key tile: wgt holds the MMA columns
+// of each 16-key step.  With one head a lane (kOwn = 1) its groups are the two
+// columns, of which this group's is taken.
+template <int D, int kOut>
+__device__ __forceinline__ void pv(float (&o)[D / 16][kOut], const uint32_t (&wgt)[4][2],
+                                   const uint8_t* tile, int gr, int g, int t4, float down) {
+  using TL = Tile<D>;
+  float acc[4][4];
+#pragma unroll
+  for (int sub = 0; sub < 4; ++sub) {
+    // word g of the group for keys 4 t4 .. 4 t4 + 3: MMA k rows 2 t4, 2 t4 + 1 and
+    // 2 t4 + 8, 2 t4 + 9
+    const uint4 v = *reinterpret_cast<const uint4*>(
+        tile + TL::v_word(0, 0, 0) + (((sub * TL::kGroups + gr) * 8 + g) * 16 + 4 * t4) * 4);
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {  // dims 2m (rows g) and 2m + 1 (rows g + 8)
+      const uint32_t sel = m | ((4 + m) << 8);  // byte m of either word, 16 bits apart
+      const uint32_t ra = __byte_perm(v.x, v.y, sel), rb = __byte_perm(v.z, v.w, sel);
+      const uint32_t a[4] = {ra & 0x000F000Fu, ra & 0x00F000F0u, rb & 0x000F000Fu,
+                             rb & 0x00F000F0u};
+      if (sub == 0) mma_codes_first(acc[m], a, wgt[sub][0], wgt[sub][1]);
+      else mma_codes(acc[m], a, wgt[sub][0], wgt[sub][1]);
+    }
+  }
+#pragma unroll
+  for (int m = 0; m < 4; ++m) {
+    float* out = o[gr * 4 + m];
+    if (kOut == 4) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) out[e] = fmaf(acc[m][e], down, out[e]);
+    } else {
+      out[0] = fmaf(acc[m][gr], down, out[0]);
+      out[1] = fmaf(acc[m][2 + gr], down, out[1]);
+    }
+  }
+}
+
+// kFew: at most four query heads a CTA.
+template <int D, bool kFew>
 __global__ void __launch_bounds__(kDecodeThreads, kCtasPerSm) decode_kernel(
     const __nv_bfloat16* __restrict__ q, Pages pg, const int* __restrict__ t,
     float* __restrict__ Opart, float2* __restrict__ MLpart, int B, int Hq, int s, int c,
     float scale_log2, int n_hg, const __grid_constant__ Theta theta) {
   using TL = Tile<D>;
   using SM = DecodeSmem<D>;
-  constexpr int kGr = TL::kGroups;
+  constexpr int kGr = TL::kGroups, kOwn = kFew ? 1 : 2;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ long long sums[kWarps];
   uint8_t* qf = smem + SM::kRings;
@@ -356,25 +394,36 @@ __global__ void __launch_bounds__(kDecodeThreads, kCtasPerSm) decode_kernel(
     __syncthreads();
   }
 
+  // A lane owns the scores of keys kr and kr + 2 of a 16-key step (MMA rows g and
+  // g + 8) and kOwn heads: 2 t4 and 2 t4 + 1, the MMA columns; or, with at most
+  // four heads, head t4, whose high part and remainder are the two columns.
   const int g = lane >> 2, t4 = lane & 3;
-  float m_run[2] = {-INFINITY, -INFINITY};  // heads 2 t4, 2 t4 + 1
-  float l_run[2];
-  uint64_t l2 = f2_pack(0.f, 0.f);          // sums of both heads
-  float off[kGr][2];                        // sum of p * offset, by group
-  // pairs of heads, rows g and g + 8; times 2^-24, rows g + 8 times 16 besides
-  uint64_t o[kGr * 4][2];
+  const int kr = 4 * (g >> 1) + (g & 1);
+  const int head0 = kFew ? t4 : 2 * t4;
+  float m_run[kOwn], l_run[kOwn];
+  float off[kGr][kOwn];       // sum of p * offset, by group
+  // O of 16 dims: rows g and g + 8, each kOwn heads; times 2^-24, rows g + 8 times
+  // 16 besides
+  float o[kGr * 4][2 * kOwn];
 #pragma unroll
-  for (int i = 0; i < kGr * 4; ++i) o[i][0] = o[i][1] = f2_pack(0.f, 0.f);
+  for (int e = 0; e < kOwn; ++e) {
+    m_run[e] = -INFINITY;
+    l_run[e] = 0.f;
 #pragma unroll
-  for (int i = 0; i < kGr; ++i) off[i][0] = off[i][1] = 0.f;
+    for (int gr = 0; gr < kGr; ++gr) off[gr][e] = 0.f;
+  }
+#pragma unroll
+  for (int i = 0; i < kGr * 4; ++i)
+#pragma unroll
+    for (int e = 0; e < 2 * kOwn; ++e) o[i][e] = 0.f;
 
   {
     // ---------------- tiles ----------------
-    const float F[2] = {qexp[2 * t4], qexp[2 * t4 + 1]};
-    const uint64_t F2 = f2_pack(F[0], F[1]);
+    float F[kOwn];
+#pragma unroll
+    for (int e = 0; e < kOwn; ++e) F[e] = qexp[head0 + e];
     // first keys of the query's own chunk and of the one before
     const int own0 = tb - tb % s, prev0 = own0 - s;
-    const int kr = 4 * (g >> 1) + (g & 1);  // MMA row g holds key kr, row g + 8 key kr + 2
     int part = 0;
     auto next_part = [&]() {  // the part just read is free: fetch another in its place
       __syncwarp();
@@ -390,12 +439,12 @@ __global__ void __launch_bounds__(kDecodeThreads, kCtasPerSm) decode_kernel(
       if (!warp_wait(full0 + 8 * buf, phase, abort_flag, 402)) break;
       const int j0 = (tile0 + it) * kTileKeys;
       const int j1 = min(j0 + kTileKeys - 1, tb);  // last valid key of the tile
-      // scores over F: [16-key step][(kr, head 0), (kr, head 1), (kr + 2, ..), ..]
-      float x[4][4];
+      // scores over F: [16-key step][key kr + 2 u, head e] at u * kOwn + e
+      float x[4][2 * kOwn];
 #pragma unroll
       for (int sub = 0; sub < 4; ++sub)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[sub][e] = 0.f;
+        for (int e = 0; e < 2 * kOwn; ++e) x[sub][e] = 0.f;
       // Scores of piece p, whose keys of the tile are p0 .. p1 - 1; in a tile of
       // several pieces the other keys take part with parameters of 0.
       auto scores = [&](auto several, int p, int p0, int p1) {
@@ -406,17 +455,24 @@ __global__ void __launch_bounds__(kDecodeThreads, kCtasPerSm) decode_kernel(
         const uint8_t* codes = ring + place;
 #pragma unroll
         for (int gr = 0; gr < kGr; ++gr) {
-          // the lane's two words of this group, high part and remainder
-          const uint4* qa = reinterpret_cast<const uint4*>(qf) +
-                            (((p * 2) * kGr + gr) * kHeads + g) * 8 + 2 * t4;
+          // column g of the lane's two words of this group: head g's high part and
+          // its remainder, or one of the two of head g / 2
+          const uint4* qa = reinterpret_cast<const uint4*>(qf) + 2 * t4 +
+                            (kFew ? (((p * 2 + (g & 1)) * kGr + gr) * kHeads + (g >> 1)) * 8
+                                  : (((p * 2) * kGr + gr) * kHeads + g) * 8);
           const uint4 h[2] = {qa[0], qa[1]};
-          const uint4 l[2] = {qa[kGr * kHeads * 8], qa[kGr * kHeads * 8 + 1]};
-          const float qs0 = qsum[(p * kHeads + 2 * t4) * kGr + gr];
-          const float qs1 = qsum[(p * kHeads + 2 * t4 + 1) * kGr + gr];
+          uint4 l[2];
+          if (!kFew) {
+            l[0] = qa[kGr * kHeads * 8];
+            l[1] = qa[kGr * kHeads * 8 + 1];
+          }
+          float qs[kOwn];
+#pragma unroll
+          for (int e = 0; e < kOwn; ++e) qs[e] = qsum[(p * kHeads + head0 + e) * kGr + gr];
 #pragma unroll
           for (int pair = 0; pair < 4; pair += kMany) {  // 16-key steps, interleaved
             uint2 wa[kMany], wb[kMany];
-            uint32_t pa[kMany], pb[kMany];
+            uint32_t par[kMany][2];
             float acc[kMany][4];
 #pragma unroll
             for (int n = 0; n < kMany; ++n) {
@@ -425,11 +481,10 @@ __global__ void __launch_bounds__(kDecodeThreads, kCtasPerSm) decode_kernel(
               const uint8_t* kp = codes + TL::k_param(0, gr) + r0 * (kGr * 4);
               wa[n] = *reinterpret_cast<const uint2*>(ka);
               wb[n] = *reinterpret_cast<const uint2*>(ka + D);
-              pa[n] = *reinterpret_cast<const uint32_t*>(kp);
-              pb[n] = *reinterpret_cast<const uint32_t*>(kp + kGr * 8);
-              if (several) {
-                if (r0 < p0 || r0 >= p1) pa[n] = 0u;
-                if (r0 + 2 < p0 || r0 + 2 >= p1) pb[n] = 0u;
+#pragma unroll
+              for (int u = 0; u < 2; ++u) {
+                par[n][u] = *reinterpret_cast<const uint32_t*>(kp + u * kGr * 8);
+                if (several && (r0 + 2 * u < p0 || r0 + 2 * u >= p1)) par[n][u] = 0u;
               }
             }
 #pragma unroll
@@ -452,24 +507,28 @@ __global__ void __launch_bounds__(kDecodeThreads, kCtasPerSm) decode_kernel(
                   a[n][3] = vv & 0x00F000F0u;
                 }
                 const uint32_t h0 = half ? h[w].z : h[w].x, h1 = half ? h[w].w : h[w].y;
-                const uint32_t l0 = half ? l[w].z : l[w].x, l1 = half ? l[w].w : l[w].y;
 #pragma unroll
                 for (int n = 0; n < kMany; ++n) {
                   if (w == 0 && half == 0) mma_codes_first(acc[n], a[n], h0, h1);
                   else mma_codes(acc[n], a[n], h0, h1);
                 }
+                if (!kFew) {
+                  const uint32_t l0 = half ? l[w].z : l[w].x, l1 = half ? l[w].w : l[w].y;
 #pragma unroll
-                for (int n = 0; n < kMany; ++n) mma_codes(acc[n], a[n], l0, l1);
+                  for (int n = 0; n < kMany; ++n) mma_codes(acc[n], a[n], l0, l1);
+                }
               }
             }
 #pragma unroll
             for (int n = 0; n < kMany; ++n)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const uint32_t w = e < 2 ? pa[n] : pb[n];
-                float& z = x[pair + n][e];
-                z = fmaf(bf16_lo(w), acc[n][e], fmaf(bf16_hi(w), (e & 1) ? qs1 : qs0, z));
-              }
+              for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int e = 0; e < kOwn; ++e) {
+                  const float sum = kFew ? acc[n][2 * u] + acc[n][2 * u + 1] : acc[n][2 * u + e];
+                  float& z = x[pair + n][u * kOwn + e];
+                  z = fmaf(bf16_lo(par[n][u]), sum, fmaf(bf16_hi(par[n][u]), qs[e], z));
+                }
           }
         }
       };
@@ -489,50 +548,53 @@ __global__ void __launch_bounds__(kDecodeThreads, kCtasPerSm) decode_kernel(
 #pragma unroll
         for (int sub = 0; sub < 4; ++sub)
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (j0 + sub * 16 + kr + (e & 2) > j1) x[sub][e] = -INFINITY;
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int e = 0; e < kOwn; ++e)
+              if (j0 + sub * 16 + kr + 2 * u > j1) x[sub][u * kOwn + e] = -INFINITY;
       }
       next_part();
-      float mx[2];
+      float mx[kOwn];
+      bool higher = false;
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        mx[e] = fmax3(fmax3(x[0][e], x[0][e + 2], x[1][e]),
-                      fmax3(x[1][e + 2], x[2][e], x[2][e + 2]), fmaxf(x[3][e], x[3][e + 2]));
+      for (int e = 0; e < kOwn; ++e) {
+        mx[e] = fmax3(fmax3(x[0][e], x[0][kOwn + e], x[1][e]),
+                      fmax3(x[1][kOwn + e], x[2][e], x[2][kOwn + e]),
+                      fmaxf(x[3][e], x[3][kOwn + e]));
 #pragma unroll
         for (int sh = 4; sh <= 16; sh <<= 1)
           mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xFFFFFFFFu, mx[e], sh));
         mx[e] *= F[e];
+        higher |= mx[e] > m_run[e];
       }
-      if (__any_sync(0xFFFFFFFFu, mx[0] > m_run[0] || mx[1] > m_run[1])) {
-        float al[2];
+      if (__any_sync(0xFFFFFFFFu, higher)) {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
+        for (int e = 0; e < kOwn; ++e) {
           const float mn = fmaxf(m_run[e], mx[e]);
-          al[e] = fast_exp2(m_run[e] - (mn == -INFINITY ? 0.f : mn));
+          const float al = fast_exp2(m_run[e] - (mn == -INFINITY ? 0.f : mn));
           m_run[e] = mn;
+          l_run[e] *= al;
 #pragma unroll
-          for (int gr = 0; gr < kGr; ++gr) off[gr][e] *= al[e];
-        }
-        const uint64_t al2 = f2_pack(al[0], al[1]);
-        l2 = f2_mul(l2, al2);
+          for (int gr = 0; gr < kGr; ++gr) off[gr][e] *= al;
 #pragma unroll
-        for (int i = 0; i < kGr * 4; ++i) {
-          o[i][0] = f2_mul(o[i][0], al2);
-          o[i][1] = f2_mul(o[i][1], al2);
+          for (int i = 0; i < kGr * 4; ++i) {
+            o[i][e] *= al;
+            o[i][kOwn + e] *= al;
+          }
         }
       }
-      const uint64_t mu2 = f2_pack(m_run[0] == -INFINITY ? 0.f : -m_run[0],
-                                   m_run[1] == -INFINITY ? 0.f : -m_run[1]);
 #pragma unroll
-      for (int sub = 0; sub < 4; ++sub)
+      for (int e = 0; e < kOwn; ++e) {
+        const float mu = m_run[e] == -INFINITY ? 0.f : -m_run[e];
 #pragma unroll
-        for (int e = 0; e < 4; e += 2) {
-          float p0, p1;
-          f2_unpack(f2_fma(f2_pack(x[sub][e], x[sub][e + 1]), F2, mu2), p0, p1);
-          x[sub][e] = fast_exp2(p0);
-          x[sub][e + 1] = fast_exp2(p1);
-          l2 = f2_add(l2, f2_pack(x[sub][e], x[sub][e + 1]));
-        }
+        for (int sub = 0; sub < 4; ++sub)
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            float& z = x[sub][u * kOwn + e];
+            z = fast_exp2(fmaf(z, F[e], mu));
+            l_run[e] += z;
+          }
+      }
       if (!warp_wait(full0 + 8 * buf, phase, abort_flag, 403)) break;
       const uint8_t* tile = ring + buf * SM::kHalf - SM::kHalf;  // V offsets count from the tile
       if (!whole) {  // rows past the sequence hold anything, NaN too
@@ -542,6 +604,11 @@ __global__ void __launch_bounds__(kDecodeThreads, kCtasPerSm) decode_kernel(
             *reinterpret_cast<uint32_t*>(const_cast<uint8_t*>(tile) + TL::v_param(r, gr)) = 0u;
         __syncwarp();
       }
+      // Weights p * scale of every 16-key step as MMA columns: the lane's two heads,
+      // a set for each group; or both groups of its one head.
+      float down[kGr];
+      uint32_t wgt[kFew ? 1 : kGr][4][2];
+      float few[kFew ? 4 : 1][2][2];
 #pragma unroll
       for (int gr = 0; gr < kGr; ++gr) {
         uint32_t par[4][2], most = 0;
@@ -559,48 +626,37 @@ __global__ void __launch_bounds__(kDecodeThreads, kCtasPerSm) decode_kernel(
         const uint32_t ex =
             max(__reduce_max_sync(0xFFFFFFFFu, most & 0xFFFFu) >> 7, 40u);
         const uint32_t up = (141u - ex) << 23;
-        const float down = __uint_as_float((ex - 14u) << 23);
-        const uint64_t down2 = f2_pack(down, down);
-        float acc[4][4];
+        down[gr] = __uint_as_float((ex - 14u) << 23);
 #pragma unroll
-        for (int sub = 0; sub < 4; ++sub) {
-          const float sa = __uint_as_float(par[sub][0] * 65536u + up);
-          const float sb = __uint_as_float(par[sub][1] * 65536u + up);
-          const float ca = bf16_hi(par[sub][0]), cb = bf16_hi(par[sub][1]);
-          const float* pr = x[sub];
+        for (int sub = 0; sub < 4; ++sub)
 #pragma unroll
-          for (int e = 0; e < 2; ++e)
-            off[gr][e] = fmaf(pr[e], ca, fmaf(pr[e + 2], cb, off[gr][e]));
-          const uint32_t b0 = transpose8x8(pack_half(pr[0] * sa, pr[1] * sa));
-          const uint32_t b1 = transpose8x8(pack_half(pr[2] * sb, pr[3] * sb));
-          // word g of the group for keys 4 t4 .. 4 t4 + 3: MMA k rows
-          // 2 t4, 2 t4 + 1 and 2 t4 + 8, 2 t4 + 9
-          const uint4 v = *reinterpret_cast<const uint4*>(
-              tile + TL::v_word(0, 0, 0) + (((sub * kGr + gr) * 8 + g) * 16 + 4 * t4) * 4);
+          for (int u = 0; u < 2; ++u) {
+            const float sc = __uint_as_float(par[sub][u] * 65536u + up);
+            const float* pr = x[sub] + u * kOwn;
 #pragma unroll
-          for (int m = 0; m < 4; ++m) {  // dims 2m (rows g) and 2m + 1 (rows g + 8)
-            const uint32_t sel = m | ((4 + m) << 8);  // byte m of either word, 16 bits apart
-            const uint32_t ra = __byte_perm(v.x, v.y, sel), rb = __byte_perm(v.z, v.w, sel);
-            const uint32_t a[4] = {ra & 0x000F000Fu, ra & 0x00F000F0u, rb & 0x000F000Fu,
-                                   rb & 0x00F000F0u};
-            if (sub == 0) mma_codes_first(acc[m], a, b0, b1);
-            else mma_codes(acc[m], a, b0, b1);
+            for (int e = 0; e < kOwn; ++e)
+              off[gr][e] = fmaf(pr[e], bf16_hi(par[sub][u]), off[gr][e]);
+            if (kFew) few[kFew ? sub : 0][u][gr] = pr[0] * sc;
+            else wgt[kFew ? 0 : gr][sub][u] = transpose8x8(pack_half(pr[0] * sc, pr[kOwn - 1] * sc));
           }
-        }
+        if (!kFew) pv<D>(o, wgt[kFew ? 0 : gr], tile, gr, g, t4, down[gr]);
+      }
+      if (kFew) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int sub = 0; sub < 4; ++sub)
 #pragma unroll
           for (int u = 0; u < 2; ++u)
-            o[gr * 4 + i][u] =
-                f2_fma(f2_pack(acc[i][2 * u], acc[i][2 * u + 1]), down2, o[gr * 4 + i][u]);
+            wgt[0][sub][u] = transpose8x8(pack_half(few[kFew ? sub : 0][u][0],
+                                                    kGr == 2 ? few[kFew ? sub : 0][u][1] : 0.f));
+#pragma unroll
+        for (int gr = 0; gr < kGr; ++gr) pv<D>(o, wgt[0], tile, gr, g, t4, down[gr]);
       }
       next_part();
     }
-    f2_unpack(l2, l_run[0], l_run[1]);
 #pragma unroll
     for (int sh = 4; sh <= 16; sh <<= 1) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
+      for (int e = 0; e < kOwn; ++e) {
         l_run[e] += __shfl_xor_sync(0xFFFFFFFFu, l_run[e], sh);
 #pragma unroll
         for (int gr = 0; gr < kGr; ++gr)
@@ -625,20 +681,17 @@ __global__ void __launch_bounds__(kDecodeThreads, kCtasPerSm) decode_kernel(
 #pragma unroll
       for (int m = 0; m < 4; ++m)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
+        for (int e = 0; e < kOwn; ++e) {
           // rows g and g + 8 are dims 2m and 2m + 1 of word g
-          float* at = mo + (warp * kHeads + 2 * t4 + e) * D + gr * 64 + 8 * g + 2 * m;
-          float lo[2], hi[2];
-          f2_unpack(o[gr * 4 + m][0], lo[0], lo[1]);
-          f2_unpack(o[gr * 4 + m][1], hi[0], hi[1]);
-          at[0] = fmaf(lo[e], 16777216.f, off[gr][e]);  // 2^24
-          at[1] = fmaf(hi[e], 1048576.f, off[gr][e]);   // 2^24 / 16
+          float* at = mo + (warp * kHeads + head0 + e) * D + gr * 64 + 8 * g + 2 * m;
+          at[0] = fmaf(o[gr * 4 + m][e], 16777216.f, off[gr][e]);        // 2^24
+          at[1] = fmaf(o[gr * 4 + m][kOwn + e], 1048576.f, off[gr][e]);  // 2^24 / 16
         }
     if (g == 0) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        mm[warp * kHeads + 2 * t4 + e] = m_run[e];
-        ml[warp * kHeads + 2 * t4 + e] = l_run[e];
+      for (int e = 0; e < kOwn; ++e) {
+        mm[warp * kHeads + head0 + e] = m_run[e];
+        ml[warp * kHeads + head0 + e] = l_run[e];
       }
     }
   }
@@ -736,7 +789,7 @@ __global__ void __launch_bounds__(kMergeThreads) decode_merge(
 }
 
 namespace {
-std::atomic<unsigned long long> g_smem_set[2];  // by head size: a bit a device
+std::atomic<unsigned long long> g_smem_set[4];  // by kernel: a bit a device
 }
 
 template <int D>
@@ -749,10 +802,11 @@ cudaError_t launch_decode_t(const void* q, const Pages& pg, const int* t, void* 
   const size_t slots = ((size_t)B * pg.Hkv * n_hg + shares) * kHeads;
   float* Opart = static_cast<float*>(workspace);
   float2* MLpart = reinterpret_cast<float2*>(Opart + slots * D);
-  auto kern = decode_kernel<D>;
+  const bool few = Hq / pg.Hkv <= 4;
+  auto kern = few ? decode_kernel<D, true> : decode_kernel<D, false>;
   constexpr int smem = DecodeSmem<D>::kTotal;
   // once a device: the attribute stays with the function there
-  std::atomic<unsigned long long>& set = g_smem_set[D / 128];
+  std::atomic<unsigned long long>& set = g_smem_set[D / 128 * 2 + few];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess && (dev >= 64 || !(set.load() >> dev & 1))) {
