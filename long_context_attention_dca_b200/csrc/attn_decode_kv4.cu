@@ -720,72 +720,83 @@ __global__ void __launch_bounds__(kDecodeThreads, kCtasPerSm) decode_kernel(
 }
 
 // O = sum_p e^{m_p - m} O_p / sum_p e^{m_p - m} l_p over the partial results of
-// a unit, LSE = m + ln(sum).  One block a (head, sequence), its eight warps over
-// the partials in turn, a row of D a warp.  It starts beside the decode kernel,
-// finds its place from t and waits for the results.
+// a unit, LSE = m + ln(sum).  kRows heads of a sequence a block, 8 / kRows warps a
+// head over its partials in turn, a row of D a warp.  It starts beside the decode
+// kernel, finds its place from t and waits for the results.
 constexpr int kMergeThreads = 256;
 
-template <int D>
+template <int D, int kRows>
 __global__ void __launch_bounds__(kMergeThreads) decode_merge(
     const float* __restrict__ Opart, const float2* __restrict__ MLpart,
     const int* __restrict__ t, __nv_bfloat16* __restrict__ O, float* __restrict__ LSE, int B,
     int Hq, int Hkv, int n_hg, long long cap, int grid_shares) {
-  constexpr int kW = kMergeThreads / 32, kEach = D / 32;
-  __shared__ float part[kW][D];
-  __shared__ float2 stat[kW];
-  __shared__ long long sums[kW];
-  const int h = blockIdx.x, b = blockIdx.y, d = threadIdx.x, warp = d >> 5, lane = d & 31;
+  constexpr int kW = kMergeThreads / 32 / kRows, kEach = D / 32;
+  __shared__ float part[kMergeThreads / 32][D];
+  __shared__ float2 stat[kMergeThreads / 32];
+  __shared__ long long sums[kMergeThreads / 32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int b = blockIdx.y, h = blockIdx.x * kRows + warp / kW;
   const int tb = __ldg(t + b);
-  const size_t row = (size_t)b * Hq + h;
   const int G = Hq / Hkv, per_seq = Hkv * n_hg;
-  const int unit = h / G * n_hg + h % G / kHeads, hh = h % G % kHeads;
   const long long all = spans_before(t, B, cap, sums) * per_seq;
+  const long long b_at = spans_before(t, b, cap, sums) * per_seq;
   const int tiles = tiles_of(tb, cap);
-  const long long g0 =
-      spans_before(t, b, cap, sums) * per_seq + (long long)unit * (tiles + kSetup) + kSetup;
   cudaGridDependencySynchronize();
-  if (tiles == 0) {
-    if (d < D) O[row * D + d] = __float2bfloat16_rn(__int_as_float(0x7fc00000));
-    if (d == 0) LSE[row] = __int_as_float(0x7fc00000);
-    return;
-  }
-  const Split split = make_split(all, share_count(all, grid_shares));
-  const long long c0 = share_of(split, g0);
-  const int n = (int)(share_of(split, g0 + tiles - 1) - c0) + 1;
-  const size_t slot0 = ((size_t)b * per_seq + unit + c0) * kHeads + hh;
-  // every warp its own partials' sum, relative to their own maximum
+  // this warp's partials' sum, relative to their own maximum
   float m = -INFINITY, l = 0.f, acc[kEach] = {};
+  if (tiles > 0 && h < Hq) {
+    const int unit = h / G * n_hg + h % G / kHeads, hh = h % G % kHeads;
+    const long long g0 = b_at + (long long)unit * (tiles + kSetup) + kSetup;
+    const Split split = make_split(all, share_count(all, grid_shares));
+    const long long c0 = share_of(split, g0);
+    const int n = (int)(share_of(split, g0 + tiles - 1) - c0) + 1;
+    const size_t slot0 = ((size_t)b * per_seq + unit + c0) * kHeads + hh;
 #pragma unroll 4
-  for (int p = warp; p < n; p += kW) {
-    const size_t slot = slot0 + (size_t)p * kHeads;
-    const float2 ml = MLpart[slot];
-    float v[kEach];
-    if (D == 128) *reinterpret_cast<float4*>(v) = reinterpret_cast<const float4*>(Opart + slot * D)[lane];
-    else *reinterpret_cast<float2*>(v) = reinterpret_cast<const float2*>(Opart + slot * D)[lane];
-    const float mn = fmaxf(m, ml.x), mu = mn == -INFINITY ? 0.f : mn;
-    const float old = fast_exp2(m - mu), now = fast_exp2(ml.x - mu);
-    m = mn;
-    l = l * old + ml.y * now;
+    for (int p = warp % kW; p < n; p += kW) {
+      const size_t slot = slot0 + (size_t)p * kHeads;
+      const float2 ml = MLpart[slot];
+      float v[kEach];
+      const float* from = Opart + slot * D + lane * kEach;
+      if (D == 128) *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(from);
+      else *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(from);
+      const float mn = fmaxf(m, ml.x), mu = mn == -INFINITY ? 0.f : mn;
+      const float old = fast_exp2(m - mu), now = fast_exp2(ml.x - mu);
+      m = mn;
+      l = l * old + ml.y * now;
 #pragma unroll
-    for (int e = 0; e < kEach; ++e) acc[e] = acc[e] * old + v[e] * now;
+      for (int e = 0; e < kEach; ++e) acc[e] = acc[e] * old + v[e] * now;
+    }
   }
+  if (kW > 1) {  // the head's warps: all sums to the first
 #pragma unroll
-  for (int e = 0; e < kEach; ++e) part[warp][lane * kEach + e] = acc[e];
-  if (lane == 0) stat[warp] = make_float2(m, l);
-  __syncthreads();
-  if (d >= D) return;
-  float M = -INFINITY, sum = 0.f, total = 0.f;
+    for (int e = 0; e < kEach; ++e) part[warp][lane * kEach + e] = acc[e];
+    if (lane == 0) stat[warp] = make_float2(m, l);
+    __syncthreads();
+    if (warp % kW) return;
+    for (int w = 1; w < kW; ++w) m = fmaxf(m, stat[warp + w].x);
+    const float mu = m == -INFINITY ? 0.f : m;
+    l = 0.f;
 #pragma unroll
-  for (int w = 0; w < kW; ++w) M = fmaxf(M, stat[w].x);
-  const float mu = M == -INFINITY ? 0.f : M;
+    for (int e = 0; e < kEach; ++e) acc[e] = 0.f;
+    for (int w = 0; w < kW; ++w) {
+      const float f = fast_exp2(stat[warp + w].x - mu);
+      l += f * stat[warp + w].y;
 #pragma unroll
-  for (int w = 0; w < kW; ++w) {
-    const float f = fast_exp2(stat[w].x - mu);
-    total += f * stat[w].y;
-    sum += f * part[w][d];
+      for (int e = 0; e < kEach; ++e) acc[e] += f * part[warp + w][lane * kEach + e];
+    }
   }
-  O[row * D + d] = __float2bfloat16_rn(sum / total);
-  if (d == 0) LSE[row] = (mu + log2f(total)) * 0.69314718055994530942f;
+  if (h >= Hq) return;
+  const float nan = __int_as_float(0x7fc00000);
+  const size_t row = (size_t)b * Hq + h;
+  uint32_t out[kEach / 2];
+#pragma unroll
+  for (int e = 0; e < kEach; e += 2)
+    out[e / 2] = tiles ? pack_bf16(acc[e] / l, acc[e + 1] / l) : pack_bf16(nan, nan);
+  __nv_bfloat16* to = O + row * D + lane * kEach;
+  if (D == 128) *reinterpret_cast<uint2*>(to) = *reinterpret_cast<const uint2*>(out);
+  else *reinterpret_cast<uint32_t*>(to) = out[0];
+  if (lane == 0)
+    LSE[row] = tiles ? ((m == -INFINITY ? 0.f : m) + log2f(l)) * 0.69314718055994530942f : nan;
 }
 
 namespace {
@@ -819,7 +830,13 @@ cudaError_t launch_decode_t(const void* q, const Pages& pg, const int* t, void* 
       scale * 1.4426950408889634f, n_hg, make_theta(D, base));
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return launch_early(decode_merge<D>, dim3(Hq, B), kMergeThreads, stream,
+  // Warps by the partials a unit has on average.  With few, a warp a head: 62
+  // sequences of 100 keys with 128 heads take 10 us, against 37 as 7936 blocks of
+  // a head each.  With many, a block a head (one sequence of 100k keys, 64 heads).
+  const long long units = (long long)B * pg.Hkv * n_hg;
+  auto merge = shares > 4 * units ? decode_merge<D, 1> : decode_merge<D, 8>;
+  const int rows = shares > 4 * units ? 1 : 8;
+  return launch_early(merge, dim3((Hq + rows - 1) / rows, B), kMergeThreads, stream,
                       static_cast<const float*>(Opart), static_cast<const float2*>(MLpart), t,
                       static_cast<__nv_bfloat16*>(O), LSE, B, Hq, pg.Hkv, n_hg, cap, shares);
 }
