@@ -450,3 +450,142 @@ def test_prompt_then_chunk_then_tokens_over_a_4bit_cache():
     assert (L4 - Lb).abs().max() <= 2.0 ** -8 * wide
     assert (O4.float() - Ob.float()).abs().max() <= (2.0 ** -7 + 2 * 2.0 ** -8 * wide) * float(
         Vall.float().abs().max())
+
+
+@pytest.mark.parametrize("D,Hq,Hkv", [(128, 6, 3), (64, 24, 2), (128, 4, 4)])
+def test_decode_of_many_short_sequences(D, Hq, Hkv):
+    # a CTA's share holds several (sequence, head) pieces; one bad page among them
+    # makes that sequence NaN and no other
+    rng = np.random.default_rng(24)
+    B, R = 150, 64
+    t = [int(x) for x in rng.integers(0, 150, B)]
+    table, num = ku.random_tables(rng, [x + 1 for x in t], R)
+    pool = ku.random_pool(rng, num, Hkv, R, D)
+    gen = torch.Generator().manual_seed(24)
+    q = ku.bf16_rows(gen, B, Hq, D)
+    want = ko.decode(ku.f64(q), pool, table, t, 37, 60)
+    dev = (q.cuda(), torch.from_numpy(pool).cuda())
+    _close(dca.dca_attn_decode_kv4_paged(*dev, ku.ints(table), ku.ints(t), 37, 60), want)
+    dca.dca_sync_status()
+    bad = 71
+    table[bad, 0] = num + 5
+    O, LSE = dca.dca_attn_decode_kv4_paged(*dev, ku.ints(table), ku.ints(t), 37, 60)
+    with pytest.raises(dca.DcaError):
+        dca.dca_sync_status()
+    assert torch.isnan(O[bad]).all() and torch.isnan(LSE[bad]).all()
+    keep = [b for b in range(B) if b != bad]
+    _close((O[keep], LSE[keep]), tuple(x[keep] for x in want))
+
+
+def test_decode_with_sequences_outside_the_cache_among_others():
+    # positions outside the cache anywhere in the batch, first and last too
+    rng = np.random.default_rng(25)
+    D, Hq, Hkv, R, B = 64, 8, 1, 64, 40
+    t = [int(x) for x in rng.integers(0, 300, B)]
+    table, num = ku.random_tables(rng, [x + 1 for x in t], R)
+    pool = ku.random_pool(rng, num, Hkv, R, D)
+    gen = torch.Generator().manual_seed(25)
+    q = ku.bf16_rows(gen, B, Hq, D)
+    want = ko.decode(ku.f64(q), pool, table, t, 50, 70)
+    out = [0, 1, 17, 18, 39]
+    tt = list(t)
+    for b, x in zip(out, (-1, 100000, table.shape[1] * R, -2 ** 31, 2 ** 31 - 1)):
+        tt[b] = x
+    O, LSE = dca.dca_attn_decode_kv4_paged(q.cuda(), torch.from_numpy(pool).cuda(),
+                                           ku.ints(table), ku.ints(tt), 50, 70)
+    with pytest.raises(dca.DcaError):
+        dca.dca_sync_status()
+    assert torch.isnan(O[out]).all() and torch.isnan(LSE[out]).all()
+    keep = [b for b in range(B) if b not in out]
+    _close((O[keep], LSE[keep]), tuple(x[keep] for x in want))
+    # none inside
+    O, LSE = dca.dca_attn_decode_kv4_paged(q.cuda(), torch.from_numpy(pool).cuda(),
+                                           ku.ints(table), ku.ints([-1] * B), 50, 70)
+    with pytest.raises(dca.DcaError):
+        dca.dca_sync_status()
+    assert torch.isnan(O).all() and torch.isnan(LSE).all()
+
+
+def test_decode_in_two_graphs_with_a_workspace_each():
+    rng = np.random.default_rng(26)
+    gen = torch.Generator().manual_seed(26)
+    D, Hq, Hkv, R, s, c = 128, 8, 2, 64, 50, 70
+    graphs = []
+    for n in (300, 1100):
+        table, num = ku.random_tables(rng, [n], R)
+        pool = ku.random_pool(rng, num, Hkv, R, D)
+        q = ku.bf16_rows(gen, 1, Hq, D)
+        dev = (q.cuda(), torch.from_numpy(pool).cuda(), ku.ints(table), ku.ints([n - 1]))
+        ws = torch.empty(dca.dca_attn_decode_kv4_workspace(1, Hq, Hkv, D, table.shape[1] * R),
+                         dtype=torch.uint8, device="cuda")
+        O, LSE = torch.empty_like(dev[0]), torch.empty(1, Hq, device="cuda")
+        call = lambda: dca.dca_attn_decode_kv4_paged(  # noqa: E731
+            *dev, s, c, workspace=ws, O=O, LSE=LSE)
+        call()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call()
+        want = ko.decode(ku.f64(q), pool, table, [n - 1], s, c)
+        graphs.append((graph, O, LSE, want, dev, ws))
+    streams = [torch.cuda.Stream() for _ in graphs]
+    for _ in range(20):  # both at once
+        for stream, (graph, O, LSE, *_) in zip(streams, graphs):
+            O.zero_()
+            LSE.zero_()
+        torch.cuda.synchronize()
+        for stream, (graph, *_) in zip(streams, graphs):
+            with torch.cuda.stream(stream):
+                graph.replay()
+        torch.cuda.synchronize()
+        for graph, O, LSE, want, *_ in graphs:
+            _close((O, LSE), want)
+    dca.dca_sync_status()
+
+
+def test_pools_past_four_gigabytes():
+    # the pages in use lie at the end of a pool of 4.7 GB, and pages are moved there
+    D, Hq, Hkv, R = 128, 4, 8, 256
+    num = 16000
+    rng = np.random.default_rng(27)
+    gen = torch.Generator().manual_seed(27)
+    small, t = 5, [600]
+    table = np.array([[num - 1, num - 3, num - 2]], np.int32)
+    part = ku.random_pool(rng, small, Hkv, R, D)
+    pool = torch.zeros((num, Hkv, R // 64, ko.tile_bytes(D)), dtype=torch.uint8, device="cuda")
+    assert pool.numel() > 2 ** 32
+    pool[-small:] = torch.from_numpy(part).cuda()
+    q = ku.bf16_rows(gen, 1, Hkv * Hq, D)
+    at = table - (num - small)
+    want = ko.decode(ku.f64(q), part, at, t, 300, 400)
+    _close(dca.dca_attn_decode_kv4_paged(q.cuda(), pool, ku.ints(table), ku.ints(t), 300, 400),
+           want)
+    k, v = ku.bf16_rows(gen, 30, Hkv, D), ku.bf16_rows(gen, 30, Hkv, D)
+    ko.append(ku.f64(k), ku.f64(v), part, at, [0, 30], [601], 300)
+    dca.dca_kv4_append_paged(k.cuda(), v.cuda(), pool, ku.ints(table), ku.ints([0, 30]),
+                             ku.ints([601]), 300, 400)
+    dca.dca_sync_status()
+    assert ku.same_pool(pool[-small:], part) is None
+    K, V = dca.dca_kv4_read_paged(pool, ku.ints(table), ku.ints([0, 30]), ku.ints([601]), 30, D)
+    got = ko.cache(part, at, 0, 631, D)
+    assert np.array_equal(ku.f64(K), ko.bf16(ko.values(*got["k"])[601:]))
+    assert np.array_equal(ku.f64(V), ko.bf16(ko.values(*got["v"])[601:]))
+    # all pages but the last ones held besides, so that a fork's copy goes to num - 4
+    refs = torch.ones(num, dtype=torch.int32, device="cuda")
+    refs[num - 4] = 0
+    both = torch.cat([ku.ints(table), torch.full_like(ku.ints(table), -1)])
+    out, counts, info = dca.dca_pages_remap(ku.ints([0, 0]), ku.ints([631, 0]),
+                                            ku.ints([631, 631]), both, refs, [pool], R)
+    assert info.tolist() == [0, 1] and out.tolist()[1] == [num - 1, num - 3, num - 4]
+    tiles = -(-(631 % R) // 64)
+    assert torch.equal(pool[num - 4, :, :tiles], pool[num - 2, :, :tiles])
+    assert torch.equal(pool[num - 4, :, tiles:].cpu(), torch.from_numpy(part[1, :, tiles:]))
+    # and compaction moves the last page to a hole at the front
+    refs = torch.ones(num, dtype=torch.int32, device="cuda")
+    refs[7] = 0
+    last = pool[-1].clone()
+    out, counts, moved, info = dca.dca_pages_compact(ku.ints([631]), ku.ints(table), refs, [pool],
+                                                     R)
+    assert info.tolist() == [num - 1, 1] and out.tolist() == [[7, num - 3, num - 2]]
+    assert torch.equal(pool[7], last) and int(moved[num - 1]) == 7
+    dca.dca_sync_status()
