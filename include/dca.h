@@ -508,9 +508,10 @@ dca_status_t dca_kv4_append_paged(const void* k_new, const void* v_new, void* po
  * [T][Hkv][D].  out_rows > 0: position p to row p of entry b of K, V
  * [B][out_rows][Hkv][D], the bf16 caches of dca_attn_prefill_varlen_chunk and
  * dca_attn_decode (a 4-bit prefix is read into a bf16 cache, extended by a
- * chunk, and the chunk's rows are appended here).  Rows of K, V that belong to
- * no position are untouched.  Offsets and table entries are checked as by
- * dca_kv4_append_paged (with out_rows > 0 the span must fit out_rows too).
+ * chunk, and the chunk's rows are appended here).  T bounds cu_seqlens in both
+ * forms.  Rows of K, V that belong to no position are untouched.  Offsets and
+ * table entries are checked as by dca_kv4_append_paged (with out_rows > 0 the
+ * span must fit out_rows too).
  * Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
 dca_status_t dca_kv4_read_paged(const void* pool, const int* block_table, int max_blocks,
                                 int block_rows, int num_blocks, const int* cu_seqlens,
@@ -526,10 +527,10 @@ size_t dca_attn_decode_kv4_workspace(int B, int Hq, int Hkv, int D, int Tcap);
  * valid, the new token's included.  O [B][Hq][D] bf16, LSE [B][Hq] fp32; s, c,
  * base, scale as dca_attn_decode.  Rows past t[b] may hold anything.  The
  * rotated query enters the scores with about 22 significant bits and the
- * codes exactly; P times the value scale is rounded to bf16.  A t[b] outside
- * the cache, or a table entry outside [0, num_blocks) that the sequence reads,
- * is reported by dca_sync_status (INVALID_ARG) and that sequence's outputs
- * are NaN.  Two calls that overlap on the GPU need a workspace each.
+ * codes exactly; P times the value scale is rounded to fp16 (11 bits, relative
+ * to the largest scale among 64 neighbouring keys).  A t[b] outside the cache,
+ * or a table entry outside [0, num_blocks) that the sequence reads, is reported
+ * by dca_sync_status (INVALID_ARG) and that sequence's outputs are NaN.  Two calls that overlap on the GPU need a workspace each.
  * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA. */
 dca_status_t dca_attn_decode_kv4_paged(const void* q, const void* pool, const int* block_table,
                                        int max_blocks, int block_rows, int num_blocks,
