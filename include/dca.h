@@ -495,7 +495,9 @@ size_t dca_kv4_tile_bytes(int D);
  * cu_seqlens, t0: DEVICE int32 [B+1], [B].  A sequence whose span is not
  * inside [0, T) or does not fit max_blocks * block_rows is skipped and
  * reported by dca_sync_status (INVALID_ARG), as is a row whose table entry lies
- * outside [0, num_blocks).  Rows of no sequence are ignored.
+ * outside [0, num_blocks).  Rows of no sequence are ignored.  No two rows of a
+ * call may go to one place: sequences that share the page they write to would
+ * mix their rows (dca_pages_remap gives each slot a last page of its own).
  * Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
 dca_status_t dca_kv4_append_paged(const void* k_new, const void* v_new, void* pool,
                                   const int* block_table, int max_blocks, int block_rows,
@@ -530,7 +532,8 @@ size_t dca_attn_decode_kv4_workspace(int B, int Hq, int Hkv, int D, int Tcap);
  * codes exactly; P times the value scale is rounded to fp16 (11 bits, relative
  * to the largest scale among 64 neighbouring keys).  A t[b] outside the cache,
  * or a table entry outside [0, num_blocks) that the sequence reads, is reported
- * by dca_sync_status (INVALID_ARG) and that sequence's outputs are NaN.  Two calls that overlap on the GPU need a workspace each.
+ * by dca_sync_status (INVALID_ARG) and that sequence's outputs are NaN.  Two
+ * calls that overlap on the GPU need a workspace each.
  * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA. */
 dca_status_t dca_attn_decode_kv4_paged(const void* q, const void* pool, const int* block_table,
                                        int max_blocks, int block_rows, int num_blocks,
@@ -550,8 +553,8 @@ typedef struct dca_page_pool {
   int unit_rows;     /* rows of a unit; divides block_rows      */
 } dca_page_pool_t;
 
-/* Workspace bytes of dca_pages_remap and dca_pages_compact.  Returns 0 for
- * unsupported arguments. */
+/* Workspace bytes of dca_pages_remap and dca_pages_compact; two calls that
+ * overlap on the GPU need one each.  Returns 0 for unsupported arguments. */
 size_t dca_pages_workspace(int B, int max_blocks, int num_blocks);
 
 /* One step of the slots over paged pools: fork, share, reorder, cut, grow and

@@ -14,6 +14,14 @@
 // Mapping: D/16 lanes own one (token, kv head) row; lane i holds dims 8i .. 8i+7
 // and their rotation partners D/2 further on, i.e. one code word of either
 // half, and its eight angles serve all kv heads the thread walks.
+//
+// What bounds it: instructions, not memory.  34816 rows of 8 heads of 128 (182 MB
+// in and out, 28 us at the copy rate) take 72 us, with an instruction issued in
+// 0.68 of the cycles: about 770 a warp for 4 rows of K and V, 24 a value, of which
+// a third each go to the rotation with its border checks and to the quantiser.
+// Packed pairs of fp32 (two elements an instruction) and the fp64 path behind
+// a test are what brought it there from 226 us.  Reading back is bound by
+// memory: the same rows take 37 us, 4.9 TB/s.
 #include "dca_common.cuh"
 #include "dca_kernels.cuh"
 #include "kv4.cuh"
@@ -21,7 +29,8 @@
 namespace dca {
 namespace kv4 {
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 64;  // small blocks fill the last wave: against 128, 23 -> 21 us for
+                              // 3525 rows of 32 heads of 64, 73 -> 72 us for the case above
 
 // A double rounded once to bf16 (nearest even): to fp32 toward zero with the
 // lost bits kept as a sticky last bit, which the second rounding cannot confuse
@@ -58,8 +67,9 @@ __device__ __forceinline__ uint32_t min_negmax(const uint32_t (&w)[4]) {
   return as_u32(__hmin2_nan(as_bf162(lo), as_bf162(hi)));
 }
 
-// Two results rounded to bf16, and where their errors (under 2.4e-7 of them)
-// leave that open: bits that differ between the roundings of the two ends.
+// Two results rounded to bf16, and where their errors leave that open: bits that
+// differ between the roundings of the two ends.  Errors below 2.9 * 2^-24 of a
+// result, and the widening's own 2^-24, fit the factors, 1 +- 4 * 2^-24.
 __device__ __forceinline__ uint32_t rounded(uint64_t y, uint32_t& open) {
   float a, b, c, d;
   f2_unpack(f2_mul(y, f2_pack(1.00000024f, 1.00000024f)), a, b);
@@ -131,33 +141,40 @@ __device__ __forceinline__ uint32_t quantise8(const uint32_t (&w)[4], const Para
   const uint64_t off2 = f2_pack(-p.off, -p.off), inv2 = f2_pack(p.inv, p.inv);
   const uint64_t neg_scale2 = f2_pack(-p.scale, -p.scale), half2 = f2_pack(0.5f, 0.5f);
   const uint64_t magic2 = f2_pack(kMagic, kMagic);
-  float c[8], far = 0.f;
+  uint64_t c2[4];
+  float far = 0.f;
 #pragma unroll
-  for (int n = 0; n < 8; n += 2) {  // two elements an instruction
-    const uint64_t x = f2_pack(bf16_lo(w[n >> 1]), bf16_hi(w[n >> 1]));
+  for (int n = 0; n < 4; ++n) {  // two elements an instruction
+    const uint64_t x = f2_pack(bf16_lo(w[n]), bf16_hi(w[n]));
     const uint64_t d = f2_fma(x, half2, off2);
     uint64_t q = f2_mul(d, inv2);
     q = f2_fma(f2_fma(q, neg_scale2, d), inv2, q);
-    const uint64_t r = f2_sub(f2_add(q, magic2), magic2);
-    f2_unpack(r, c[n], c[n + 1]);
+    c2[n] = f2_sub(f2_add(q, magic2), magic2);
     float r0, r1;
-    f2_unpack(f2_fma(r, neg_scale2, d), r0, r1);
+    f2_unpack(f2_fma(c2[n], neg_scale2, d), r0, r1);
     far = fmax3(far, fabsf(r0), fabsf(r1));
   }
   const float half = 0.5f * p.scale;
-  // Only a value far below the offset makes d inexact, which matters on a border.
-  const __nv_bfloat162 least =
-      __hmin2(__hmin2(__habs2(as_bf162(w[0])), __habs2(as_bf162(w[1]))),
-              __hmin2(__habs2(as_bf162(w[2])), __habs2(as_bf162(w[3]))));
-  const bool small = fminf(bf16_lo(as_u32(least)), bf16_hi(as_u32(least))) <
-                     fabsf(p.off) * 1.220703125e-4f;  // 2^-13 of half the offset
-  // (no scale: a constant group or one that is not finite, codes 0; an infinite
-  // reciprocal: a subnormal scale)
-  if (half > 0.f && (far > half || (small && far == half) || p.inv == INFINITY))
-    return mend_codes(make_uint4(w[0], w[1], w[2], w[3]), p.off, p.scale);
-  const float lo = fmaf(c[3], 4096.f, fmaf(c[2], 256.f, fmaf(c[1], 16.f, c[0])));
-  const float hi = fmaf(c[7], 4096.f, fmaf(c[6], 256.f, fmaf(c[5], 16.f, c[4])));
-  return __float2uint_rz(lo) | (__float2uint_rz(hi) << 16);
+  if (half > 0.f && (far >= half || p.inv == INFINITY)) {
+    // Only a value far below the offset makes d inexact, which matters on a border.
+    const __nv_bfloat162 least =
+        __hmin2(__hmin2(__habs2(as_bf162(w[0])), __habs2(as_bf162(w[1]))),
+                __hmin2(__habs2(as_bf162(w[2])), __habs2(as_bf162(w[3]))));
+    const bool small = fminf(bf16_lo(as_u32(least)), bf16_hi(as_u32(least))) <
+                       fabsf(p.off) * 1.220703125e-4f;  // 2^-13 of half the offset
+    // (an infinite reciprocal: a subnormal scale)
+    if (far > half || small || p.inv == INFINITY)
+      return mend_codes(make_uint4(w[0], w[1], w[2], w[3]), p.off, p.scale);
+  }
+  // c0 + 16 c1 + 256 c2 + 4096 c3 on 2^23, whose low half is the integer
+  float a0, a1, b0, b1, lo, hi;
+  const uint64_t by256 = f2_pack(256.f, 256.f);
+  f2_unpack(f2_fma(c2[1], by256, c2[0]), a0, a1);
+  f2_unpack(f2_fma(c2[3], by256, c2[2]), b0, b1);
+  lo = fmaf(a1, 16.f, a0 + 8388608.f);
+  hi = fmaf(b1, 16.f, b0 + 8388608.f);
+  // (no scale: a constant group, or one that is not finite, whose sums are NaN)
+  return half > 0.f ? __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x5410) : 0u;
 }
 
 // Packed row r: its sequence b and absolute index, or b = -1 for a row of no
@@ -275,10 +292,11 @@ __global__ void __launch_bounds__(kThreads) append_kernel(
                                    f2_fma(q2, c.y, f2_mul(p2, sn.y)));
         k[0][n] = rounded(o0, b0);
         k[1][n] = rounded(o1, b1);
-        // A result far below its operands has a larger error than its own size
-        // tells: that is a border too.
+        // The errors are 2^-24 of the first sum, 3 * 2^-39 of the operands for the
+        // second and 2^-24 for the last addition: under 2.76 * 2^-24 of a result that
+        // is above 2^-13 of its operands.  One below that is a border too.
         const __nv_bfloat162 size = __hadd2(__habs2(as_bf162(a[n])), __habs2(as_bf162(b[n])));
-        const __nv_bfloat162 much = __float2bfloat162_rn(4096.f);
+        const __nv_bfloat162 much = __float2bfloat162_rn(8192.f);
         b0 |= as_u32(__hsub2(__hmul2(__habs2(as_bf162(k[0][n])), much), size)) & 0x80008000u;
         b1 |= as_u32(__hsub2(__hmul2(__habs2(as_bf162(k[1][n])), much), size)) & 0x80008000u;
         if (b0 | b1) again |= 1u << n;
@@ -377,7 +395,8 @@ __device__ __forceinline__ void dequantise8(uint32_t w, uint32_t param, uint32_t
 // [B][out_rows][Hkv][D].  code * scale + offset is formed in fp32, where it is
 // exact unless the offset is over 2^11 steps away, and rounded once.
 // One block a (run of rows, kv head), so that it reads whole tiles; a thread
-// takes kReadRows rows of the run, all their loads in flight at once.
+// takes kReadRows rows of the run, all their loads in flight at once (one row: 43 us
+// for the case above; two: 37).
 constexpr int kReadRows = 2;
 
 template <int D>
@@ -438,7 +457,8 @@ __global__ void __launch_bounds__(kThreads) read_kernel(
 }
 
 // Heads of a block: what a thread works out for its row serves them all, so as
-// many as leave 4 blocks an SM.
+// many as leave 4 blocks an SM (3525 rows of 32 heads of 64: 27 us with 2 blocks
+// an SM, 21 with 4, 23 with 8).
 inline int heads_per_block(long long row_blocks, int Hkv) {
   int n = Hkv;
   while (n > 1 && row_blocks * ((Hkv + n - 1) / n) < 148 * 4) n = (n + 1) / 2;
@@ -449,7 +469,7 @@ template <int D>
 cudaError_t launch_append_t(const void* k_new, const void* v_new, const Pages& pg, const int* cu,
                             const int* t0, int B, int T, int s, float base, cudaStream_t stream) {
   constexpr int kRows = kThreads / (D / 16);
-  const unsigned gx = (unsigned)((T + kRows - 1) / kRows);
+  const unsigned gx = (unsigned)(((long long)T + kRows - 1) / kRows);
   const int hpc = heads_per_block(gx, pg.Hkv);
   const unsigned gy = (unsigned)((pg.Hkv + hpc - 1) / hpc);
   append_kernel<D><<<dim3(gx + 1, gy), kThreads, 0, stream>>>(

@@ -116,6 +116,31 @@ def test_append_of_unusual_values(D):
     assert ku.same_pool(got, want) is None
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_append_of_keys_that_cancel_or_leave_the_normal_range(D):
+    # pairs whose rotation nearly vanishes: p = q tan(angle) rounded to bf16 leaves
+    # 2^-9 of the operands at most, and now and then 2^-13 and far less
+    gen = torch.Generator().manual_seed(15)
+    n, Hkv, t0, s = 700, 2, 40, 5000
+    k = ku.bf16_rows(gen, n, Hkv, D)
+    pos = torch.arange(t0, t0 + n, dtype=torch.float64)[:, None]
+    theta = 10000.0 ** (-2.0 * torch.arange(D // 2, dtype=torch.float64) / D)
+    tan = torch.tan(pos * theta)[:, None, :]
+    q = k[..., D // 2:].double()
+    p = torch.where(tan.abs() < 1e4, q * tan, q)
+    k[..., :D // 2] = p.to(torch.bfloat16)
+    got, want, *_ = _append_case(15, [n], [t0], Hkv, D, 64, s, k=k)
+    assert ku.same_pool(got, want) is None
+    # subnormals, sums next to them and next to the largest bf16
+    k = torch.randn(120, Hkv, D, generator=gen)
+    for i, size in enumerate((1e-30, 1e-36, 1e-37, 1e-38, 3e-39, 1e-39, 1e-40, 6e-41, 1e37, 5e37,
+                              1e38, 1.7e38)):
+        k[i * 10:i * 10 + 10] *= size
+    k = k.clamp(-3.38e38, 3.38e38).to(torch.bfloat16)
+    got, want, *_ = _append_case(16, [120], [t0], Hkv, D, 64, s, k=k, v=k.clone())
+    assert ku.same_pool(got, want) is None
+
+
 def test_append_ignores_rows_of_no_sequence_and_keeps_the_rest():
     # _append_case compares whole pools, random bytes elsewhere included
     got, want, *_ = _append_case(6, [9, 20], [60, 1], 2, 128, 64, 10, pad=77)
