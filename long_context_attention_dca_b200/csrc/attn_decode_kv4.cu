@@ -50,7 +50,7 @@ constexpr int kMaxTiles = 512;  // of a CTA's share, so that their places fit in
 // end of one unit and the beginning of the next; each piece gives a partial
 // result.  Share c of unit U writes slot U + c: along the line of tiles each new
 // piece raises one of the two, so no slot is used twice.
-constexpr int kSetup = 12;
+constexpr int kSetup = 8;
 struct Split {
   long long shares, each, extra;  // the first `extra` shares hold one tile more
 };
@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(kDecodeThreads, kCtasPerSm) decode_kernel(
   for (int i = tid; i < SM::kQ / 16; i += kDecodeThreads)  // heads a unit does not have
     reinterpret_cast<uint4*>(qf)[i] = make_uint4(0, 0, 0, 0);
   for (int i = tid; i < 3 * kHeads * kGr + kHeads; i += kDecodeThreads) qsum[i] = 0.f;
-  int turned = -1;  // the sequence whose rotations cs holds
+  int turned = -1;  // the sequence and DCA pieces whose rotations cs holds
 
   for (int piece = 0; at < end; ++piece) {
   volatile int* bad_page = bad_pages + (piece & 1);
@@ -300,14 +300,34 @@ __global__ void __launch_bounds__(kDecodeThreads, kCtasPerSm) decode_kernel(
   const int n_heads = min(kHeads, G - hg * kHeads);
   __syncthreads();  // the piece before is done
   if (tid == 0) bad_pages[~piece & 1] = 0;
-  // everything the piece begins with, in flight at once: its pages, its queries
+  // first keys of the query's own chunk and of the one before; the DCA pieces that
+  // the share's keys lie in, p_lo for the last key and p_hi for the first
+  const int own0 = tb - tb % s, prev0 = own0 - s;
+  auto dca_piece = [&](int j) { return j < prev0 ? 2 : (j < own0 ? 1 : 0); };
+  const int p_lo = dca_piece(min(tile1 * kTileKeys - 1, tb)), p_hi = dca_piece(tile0 * kTileKeys);
+  // everything that is fetched to begin with, in flight at once behind the rotations:
+  // the first of the pages and the queries
+  const int* pages = pg.table + (size_t)seq * pg.max_blocks;
+  int blk = tid < n_tiles ? __ldg(pages + (tile0 + tid) / tpb) : 0;
   const bool has_q = tid < n_heads * D / 8;
   uint4 q8 = {};
   if (has_q)
     q8 = __ldg(reinterpret_cast<const uint4*>(q + ((size_t)seq * Hq + h_base) * D) + tid);
+  const int turn = (seq * 3 + p_lo) * 3 + p_hi;
+  if (turned != turn) {
+    const int im = tb % s;
+#pragma unroll 1
+    for (int x = p_lo * (D / 2) + tid; x < (p_hi + 1) * (D / 2); x += kDecodeThreads) {
+      const int p = x / (D / 2), k = x % (D / 2);
+      double cd, sd;
+      sincos64((double)query_pos_for_piece(p, im, s, c) * theta.v[k], cd, sd);
+      cs[x] = make_float2((float)cd, (float)sd);
+    }
+    turned = turn;
+  }
   for (int i = tid; i < n_tiles; i += kDecodeThreads) {
     const int tile = tile0 + i;
-    int blk = __ldg(pg.table + (size_t)seq * pg.max_blocks + tile / tpb);
+    if (i != tid) blk = __ldg(pages + tile / tpb);
     if ((unsigned)blk >= (unsigned)pg.num_blocks) {
       report_error(kDevBadArg, 208);  // the outputs become NaN
       *bad_page = 1;
@@ -316,17 +336,6 @@ __global__ void __launch_bounds__(kDecodeThreads, kCtasPerSm) decode_kernel(
     places[i] = (uint32_t)(((size_t)blk * pg.Hkv + hk) * tpb + tile % tpb);
   }
   if (has_q) reinterpret_cast<uint4*>(qraw)[tid] = q8;
-  if (turned != seq) {
-    const int im = tb % s;
-#pragma unroll 1
-    for (int x = tid; x < 3 * (D / 2); x += kDecodeThreads) {
-      const int p = x / (D / 2), k = x % (D / 2);
-      double cd, sd;
-      sincos64((double)query_pos_for_piece(p, im, s, c) * theta.v[k], cd, sd);
-      cs[x] = make_float2((float)cd, (float)sd);
-    }
-    turned = seq;
-  }
   __syncthreads();
   const int parts = n_tiles > warp ? 2 * ((n_tiles - warp + kWarps - 1) / kWarps) : 0;
   // lane 0: fetch part i of this warp's tiles into buffer `to`
@@ -341,12 +350,12 @@ __global__ void __launch_bounds__(kDecodeThreads, kCtasPerSm) decode_kernel(
     for (int i = 0, to = buf; i < min(parts, kRing); ++i, to = to == kRing - 1 ? 0 : to + 1)
       fetch(i, to);
 
-  // ---------------- queries: three rotations, fragments, group sums ----------------
+  // ---------------- queries: rotations, fragments, group sums ----------------
   {
     constexpr int kPairs = D / 64;  // (k, k + D/2) pairs a lane owns of a head
 #pragma unroll 1
-    for (int job = warp; job < 3 * n_heads; job += kWarps) {  // a head and a piece
-      const int hh = job / 3, p = job % 3;
+    for (int job = warp; job < (p_hi - p_lo + 1) * n_heads; job += kWarps) {
+      const int p = p_lo + job / n_heads, hh = job % n_heads;  // a piece and a head
       float x0[kPairs], x1[kPairs], big = 0.f;
 #pragma unroll
       for (int u = 0; u < kPairs; ++u) {
@@ -389,7 +398,7 @@ __global__ void __launch_bounds__(kDecodeThreads, kCtasPerSm) decode_kernel(
         const float unit = down * down2 * 5.9604644775390625e-8f;  // 2^-24
         if (lane < kGr) qsum[(p * kHeads + hh) * kGr + lane] = (lane == 0 ? sum[0] : sum[1]) * unit;
       }
-      if (lane == 0 && p == 0) qexp[hh] = ldexpf(1.f, e + 24);
+      if (lane == 0 && p == p_lo) qexp[hh] = ldexpf(1.f, e + 24);
     }
     __syncthreads();
   }
@@ -422,8 +431,6 @@ __global__ void __launch_bounds__(kDecodeThreads, kCtasPerSm) decode_kernel(
     float F[kOwn];
 #pragma unroll
     for (int e = 0; e < kOwn; ++e) F[e] = qexp[head0 + e];
-    // first keys of the query's own chunk and of the one before
-    const int own0 = tb - tb % s, prev0 = own0 - s;
     int part = 0;
     auto next_part = [&]() {  // the part just read is free: fetch another in its place
       __syncwarp();
@@ -532,8 +539,7 @@ __global__ void __launch_bounds__(kDecodeThreads, kCtasPerSm) decode_kernel(
           }
         }
       };
-      const int first = j1 < prev0 ? 2 : (j1 < own0 ? 1 : 0);  // piece of the last key
-      const int last = j0 < prev0 ? 2 : (j0 < own0 ? 1 : 0);   // and of the first one
+      const int first = dca_piece(j1), last = dca_piece(j0);  // of the last key, the first one
       const bool whole = j1 - j0 == kTileKeys - 1;
       if (first == last && whole) {
         scores(std::false_type(), first, 0, kTileKeys);
