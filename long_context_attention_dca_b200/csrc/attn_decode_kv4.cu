@@ -24,6 +24,17 @@
 // and the update of O are paid once per 64 keys of a warp.  The sequence's
 // tiles are shared out evenly on the device from t[b], whatever the cache's
 // capacity.  Kernel 2 merges the shares.
+//
+// What bounds it.  A key costs 144 bytes of cache a kv head (D = 128) and, with
+// eight query heads on it, about 17 instructions a warp (1065 for 64 keys, 96 of
+// them matrix products, half of the rest unpacking nibbles).  With one query
+// head memory bounds it: 24 sequences of 16k keys, 32 kv heads, take 290 us,
+// 6.1 TB/s, 93 % of the copy rate.  With eight, the instructions do: 16 sequences
+// of 33k to 65k keys, 8 kv heads, take 200 us, 4.5 TB/s, of which the loads alone
+// take 143 and the arithmetic on data held in L2 192; the logic pipe is busy for
+// 52 % and the matrix pipe for 38 %, the rest is fixed latency between them.  One
+// sequence of 100k keys takes 43 us against 17.6 of bytes: 12 us pass before the
+// first and after the last tile, and seven or eight tiles a warp follow.
 #include <atomic>
 
 #include "dca_common.cuh"
@@ -35,11 +46,16 @@ namespace dca {
 namespace kv4 {
 
 constexpr int kHeads = 8;   // query heads per CTA (MMA N)
-constexpr int kWarps = 4;   // per CTA, each with a ring of its own
-constexpr int kRing = 3;    // half tiles (K or V part) of a ring
+// Three CTAs of four warps an SM, a ring of three half tiles (K or V part) a
+// warp: 64.5 us for 24 x 4k keys of 32 kv heads, 50 for 1 x 100k and 202 for 16 x
+// 64k of 8.  Two CTAs with rings of four took 66, 46 and 208, two of six warps 69,
+// 47 and 212, one of twelve 87, 48 and 235.
+constexpr int kWarps = 4;
+constexpr int kRing = 3;
 constexpr int kDecodeThreads = kWarps * 32;
 constexpr int kCtasPerSm = 3;
-constexpr int kMany = 2;    // 16-key steps whose score products run interleaved
+constexpr int kMany = 2;    // 16-key steps whose score products run interleaved: 1 takes 204 us
+                            // for the last of those, 2 takes 200
 constexpr int kMaxTiles = 512;  // of a CTA's share, so that their places fit in shared memory
 
 // Work.  A unit is a (sequence, kv head, group of <= 8 query heads).  The tiles
@@ -49,7 +65,9 @@ constexpr int kMaxTiles = 512;  // of a CTA's share, so that their places fit in
 // one (rotating the queries, the first fetch, the merge).  A share may hold the
 // end of one unit and the beginning of the next; each piece gives a partial
 // result.  Share c of unit U writes slot U + c: along the line of tiles each new
-// piece raises one of the two, so no slot is used twice.
+// piece raises one of the two, so no slot is used twice.  Over 22 batches of 1 to
+// 40 sequences of 1k to 30k keys, a setup of 6, 8, 9, 10 and 12 tiles differed by
+// at most 1.4 % in the mean, 8 the fastest.
 constexpr int kSetup = 8;
 struct Split {
   long long shares, each, extra;  // the first `extra` shares hold one tile more
@@ -206,7 +224,9 @@ __device__ __forceinline__ void pv(float (&o)[D / 16][kOut], const uint32_t (&wg
   }
 }
 
-// kFew: at most four query heads a CTA.
+// kFew: at most four query heads a kv head.  Eight MMA columns then hold both
+// parts of every query, half the score products: 66 us for 24 x 4k keys of 32 kv
+// heads with a query head each, against 77 as eight columns of high parts.
 template <int D, bool kFew>
 __global__ void __launch_bounds__(kDecodeThreads, kCtasPerSm) decode_kernel(
     const __nv_bfloat16* __restrict__ q, Pages pg, const int* __restrict__ t,
