@@ -7,8 +7,12 @@
 // exact as fp16 SUBNORMALS: a nibble masked into the low mantissa bits of each
 // half of a word is c * 2^-24 (bits 4-7: 16 c * 2^-24, undone by a query
 // pre-scaled by 1/16), so eight codes cost four logic operations and a shift.
-// q is kept as an fp16 high part and remainder (normalised per head by a power
-// of two), about 22 significant bits.  For the values,
+// q, scaled per head by a power of two to below 2^11, is kept as its nearest
+// integers and the fp16 remainders: 22 bits and more of the head's largest.  The
+// products of the integers are integers below 2^21, so their sum is exact; those
+// of the remainders are summed apart.  (Rounded to fp16 and summed as one, the
+// sums, whose codes are not centred, lost up to 1e-5 of a score to the tensor
+// core's truncation.)  For the values,
 //     O = sum_j (p_j scale_j) c_j + sum_j p_j offset_j,
 // again on the bare codes, with p_j scale_j rounded to fp16 after a
 // normalisation by the largest scale of the 64-key tile (a power of two), so
@@ -26,13 +30,13 @@
 // capacity.  Kernel 2 merges the shares.
 //
 // What bounds it.  A key costs 144 bytes of cache a kv head (D = 128) and, with
-// eight query heads on it, about 17 instructions a warp (1065 for 64 keys, 96 of
+// eight query heads on it, about 17 instructions a warp (1100 for 64 keys, 96 of
 // them matrix products, half of the rest unpacking nibbles).  With one query
 // head memory bounds it: 24 sequences of 16k keys, 32 kv heads, take 290 us,
 // 6.1 TB/s, 93 % of the copy rate.  With eight, the instructions do: 16 sequences
-// of 33k to 65k keys, 8 kv heads, take 200 us, 4.5 TB/s, of which the loads alone
-// take 143 and the arithmetic on data held in L2 192; the logic pipe is busy for
-// 52 % and the matrix pipe for 38 %, the rest is fixed latency between them.  One
+// of 33k to 65k keys, 8 kv heads, take 204 us, 4.4 TB/s, where the loads alone
+// take 143; the logic pipe is busy for half of it and the matrix pipe for 38 %, the
+// rest is fixed latency between them.  One
 // sequence of 100k keys takes 43 us against 17.6 of bytes: 12 us pass before the
 // first and after the last tile, and seven or eight tiles a warp follow.
 #include <atomic>
@@ -54,8 +58,8 @@ constexpr int kWarps = 4;
 constexpr int kRing = 3;
 constexpr int kDecodeThreads = kWarps * 32;
 constexpr int kCtasPerSm = 3;
-constexpr int kMany = 2;    // 16-key steps whose score products run interleaved: 1 takes 204 us
-                            // for the last of those, 2 takes 200
+constexpr int kMany = 2;    // 16-key steps whose score products run interleaved: 208 us with one
+                            // for the last of those, 204 with two
 constexpr int kMaxTiles = 512;  // of a CTA's share, so that their places fit in shared memory
 
 // Work.  A unit is a (sequence, kv head, group of <= 8 query heads).  The tiles
@@ -385,8 +389,8 @@ __global__ void __launch_bounds__(kDecodeThreads, kCtasPerSm) decode_kernel(
       }
 #pragma unroll
       for (int sh = 16; sh >= 1; sh >>= 1) big = fmaxf(big, __shfl_xor_sync(~0u, big, sh));
-      // every rotated value times 2^-e stays below 2^13
-      const int e = big > 0.f ? (int)(__float_as_uint(big) >> 23) - 127 - 12 : 0;
+      // every rotated value times 2^-e stays below 2^11
+      const int e = big > 0.f ? (int)(__float_as_uint(big) >> 23) - 127 - 10 : 0;
       const float down = ldexpf(1.f, -(e / 2)), down2 = ldexpf(1.f, -(e - e / 2));
       {
         float sum[2] = {0.f, 0.f};
@@ -402,9 +406,9 @@ __global__ void __launch_bounds__(kDecodeThreads, kCtasPerSm) decode_kernel(
             // nibbles 0..3 of a word go to the low halves of four registers,
             // 4..7 to the high halves; odd nibbles arrive times 16
             const int g = d / 64, i = (d % 64) / 8, n = d % 8;
-            const float z = y[v] * down * down2 * ((n & 1) ? 0.0625f : 1.f);
-            const __half hi = __float2half_rn(z);
-            const __half lo = __float2half_rn(z - __half2float(hi));
+            const float z = y[v] * down * down2, whole = rintf(z), by = (n & 1) ? 0.0625f : 1.f;
+            const __half hi = __float2half_rn(whole * by);
+            const __half lo = __float2half_rn((z - whole) * by);
             const int at = ((((p * 2) * kGr + g) * kHeads + hh) * 8 + i) * 8 + (n & 3) * 2 + (n >> 2);
             reinterpret_cast<__half*>(qf)[at] = hi;
             reinterpret_cast<__half*>(qf)[at + kGr * kHeads * 64] = lo;
@@ -500,7 +504,7 @@ __global__ void __launch_bounds__(kDecodeThreads, kCtasPerSm) decode_kernel(
           for (int pair = 0; pair < 4; pair += kMany) {  // 16-key steps, interleaved
             uint2 wa[kMany], wb[kMany];
             uint32_t par[kMany][2];
-            float acc[kMany][4];
+            float acc[kMany][4], low[kFew ? 1 : kMany][4];
 #pragma unroll
             for (int n = 0; n < kMany; ++n) {
               const int r0 = (pair + n) * 16 + kr;
@@ -542,7 +546,10 @@ __global__ void __launch_bounds__(kDecodeThreads, kCtasPerSm) decode_kernel(
                 if (!kFew) {
                   const uint32_t l0 = half ? l[w].z : l[w].x, l1 = half ? l[w].w : l[w].y;
 #pragma unroll
-                  for (int n = 0; n < kMany; ++n) mma_codes(acc[n], a[n], l0, l1);
+                  for (int n = 0; n < kMany; ++n) {
+                    if (w == 0 && half == 0) mma_codes_first(low[kFew ? 0 : n], a[n], l0, l1);
+                    else mma_codes(low[kFew ? 0 : n], a[n], l0, l1);
+                  }
                 }
               }
             }
@@ -552,7 +559,8 @@ __global__ void __launch_bounds__(kDecodeThreads, kCtasPerSm) decode_kernel(
               for (int u = 0; u < 2; ++u)
 #pragma unroll
                 for (int e = 0; e < kOwn; ++e) {
-                  const float sum = kFew ? acc[n][2 * u] + acc[n][2 * u + 1] : acc[n][2 * u + e];
+                  const float sum = kFew ? acc[n][2 * u] + acc[n][2 * u + 1]
+                                         : acc[n][2 * u + e] + low[kFew ? 0 : n][2 * u + e];
                   float& z = x[pair + n][u * kOwn + e];
                   z = fmaf(bf16_lo(par[n][u]), sum, fmaf(bf16_hi(par[n][u]), qs[e], z));
                 }

@@ -169,10 +169,14 @@ def cache(pool, table, b, n, D):
 
 def decode(q, pool, table, t, s, c, base=10000.0, scale=0.0):
     """(O, LSE, bound_O, bound_LSE): the attention, and how far a kernel may be
-    from it.  bound_O: P times the value scale and the output are each rounded
-    to bf16 (half a step is 2^-8 of the value), fp32 sums besides.  bound_LSE:
-    the largest error a score can have from fp32 sums over D products and a
-    query of 22 bits, and the fp32 sum of the exponentials."""
+    from it.  bound_O: the output is rounded to bf16 (half a step is 2^-8 of it).
+    Every weight P times the value scale, which multiplies a code of 0 .. 15, is
+    rounded to fp16 (half a step is 2^-11 of it) after a normalisation that puts
+    the largest scale of a group among the 64 keys of a tile between 2^14 and
+    2^15: below fp16's normal range half a step is 2^-25, which is 2^-39 of that
+    scale, times a code of 15.  fp32 sums of codes and offsets besides.
+    bound_LSE: the largest error a score can have from fp32 sums over D products
+    and a query of 22 bits, and the fp32 sum of the exponentials."""
     B, Hq, D = q.shape
     Hkv = pool.shape[1]
     sc = scale if scale else 1.0 / np.sqrt(D)
@@ -190,8 +194,10 @@ def decode(q, pool, table, t, s, c, base=10000.0, scale=0.0):
             qr = {p: orc.rotate(q[b, h], p, base) for p in set(pos.tolist())}
             z = np.array([qr[p] @ key[j, hk] for j, p in enumerate(pos.tolist())]) * sc
             w = np.exp(z - LSE[b, h])
-            part = np.repeat(vs, 64, 1) * np.abs(codes - 8.0)
-            whole = part + np.repeat(np.abs(vo + 8 * vs), 64, 1)
+            part = np.repeat(vs, 64, 1) * codes
+            whole = part + np.repeat(np.abs(vo), 64, 1)
+            least = sum(len(x) * x.max(0) for x in np.split(vs, range(64, i + 1, 64)))
+            least = np.repeat(least, 64) * 15 * 2.0 ** -39
             # errors of the scores change every weight by as much, relatively
             kc, ks, ko = (x[:, hk] for x in got["k"])
             size = np.repeat(np.abs(ko), 64, 1) + np.repeat(ks, 64, 1) * kc
@@ -199,8 +205,8 @@ def decode(q, pool, table, t, s, c, base=10000.0, scale=0.0):
             err = abs(sc) * (D + 16) * 2.0 ** -23 * qa * size.sum(1).max()
             sums = (16 + (i + 1) / 64) * 2.0 ** -23
             bL[b, h] = err + sums + abs(LSE[b, h]) * 2.0 ** -22
-            bO[b, h] = 2.0 ** -8 * np.abs(O[b, h]) + 2.0 ** -8 * (w @ part) + (
-                2 * err + 2 * sums) * (w @ whole) + 1e-30
+            bO[b, h] = 2.0 ** -8 * np.abs(O[b, h]) + 2.0 ** -11 * (w @ part) + (
+                2 * err + 2 * sums) * (w @ whole) + least + 1e-30
     return O, LSE, bO, bL
 
 

@@ -4,8 +4,8 @@ plain fp64 restatement.
 Append is held to equality, byte for byte: its roundings are those of the exact
 result, which the oracle forms in fp64 (an element nearer to a border than fp64
 can tell would need a coincidence of about 1e-12).  Decode is held to the
-oracle's own bounds: a bf16 rounding of P times the value scale and one of the
-output, and fp32 arithmetic besides.
+oracle's own bounds: an fp16 rounding of P times the value scale, a bf16 one of
+the output, and fp32 arithmetic besides.
 """
 
 import numpy as np
@@ -263,6 +263,32 @@ def _close(got, want, what=""):
 ])
 def test_decode_matches_the_oracle(D, Hq, Hkv, R, t, s, c):
     _close(*_decode_case(10, D, Hq, Hkv, R, t, s, c))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("G", [1, 4, 5, 8, 12])
+def test_decode_of_a_few_keys_keeps_fp32_scores(D, G):
+    # With one to four keys LSE is a score or nearly one, of size about 1 for normal
+    # q and k.  Its roundings, each of 2^-24 / sqrt(3) rms of what it rounds, are:
+    # three for every rotated element (6e-8 of the score in all); 64 in each of the
+    # six levels of a group's sum of q, of 64 / 2^n elements of size sqrt(2^n) (8 * sqrt(6)
+    # * 3.4e-8 = 7e-7, times an offset of 2.5 over sqrt(128): 1.5e-7, sqrt(2) of that
+    # for two groups); some six of the products scale * sum(q c) and offset * sum(q), of
+    # size 2 each (2e-7).  The integer parts of the query sum exactly and their
+    # remainders are 2^-11 of them.  Together 3.5e-7 rms; 1e-6 is allowed.
+    rng, gen = np.random.default_rng(31), torch.Generator().manual_seed(31)
+    B, Hkv, R, s = 24, 4, 64, 3
+    t = [b % 4 for b in range(B)]
+    lens = [x + 1 for x in t]
+    k, v = (torch.randn(sum(lens), Hkv, D, generator=gen).bfloat16() for _ in range(2))
+    table, num = ku.random_tables(rng, lens, R)
+    pool = np.zeros((num, Hkv, 1, ko.tile_bytes(D)), np.uint8)
+    ko.append(ku.f64(k), ku.f64(v), pool, table, _cu(lens), [0] * B, s)
+    q = torch.randn(B, Hkv * G, D, generator=gen).bfloat16()
+    (O, LSE), want = _decode_case(31, D, Hkv * G, Hkv, R, t, s, 5, q=q, pool=pool, table=table)
+    _close((O, LSE), want)
+    off = ku.f64(LSE) - want[1]
+    assert np.sqrt((off ** 2).mean()) <= 1e-6 * np.sqrt((want[1] ** 2).mean())
 
 
 @pytest.mark.parametrize("D", [64, 128])

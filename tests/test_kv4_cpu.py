@@ -186,10 +186,10 @@ def test_tile_and_workspace_sizes(lib):
     assert dca.dca_attn_decode_kv4_workspace(0, 8, 1, 128, 64) == 0
     # a slot of 8 heads x (D + 2) floats for every unit (sequence, kv head, 8
     # query heads) and every share; a share is four tiles, a unit its tiles and
-    # 12 more, and there are 3 shares an SM at most unless one passes 512 tiles
+    # 8 more, and there are 3 shares an SM at most unless one passes 512 tiles
     def slots(B, Hkv, groups, Tcap):
         units = B * Hkv * groups
-        tiles = units * (-(-Tcap // 64) + 12)
+        tiles = units * (-(-Tcap // 64) + 8)
         return units + max(1, min(tiles // 4, max(148 * 3, -(-tiles // 512))))
 
     for B, Hq, Hkv, D, Tcap in ((1, 8, 1, 128, 64), (1, 8, 1, 64, 129), (16, 64, 8, 128, 65536),
