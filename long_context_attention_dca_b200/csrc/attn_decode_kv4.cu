@@ -37,7 +37,7 @@
 // of 33k to 65k keys, 8 kv heads, take 204 us, 4.4 TB/s, where the loads alone
 // take 143; the logic pipe is busy for half of it and the matrix pipe for 38 %, the
 // rest is fixed latency between them.  One
-// sequence of 100k keys takes 43 us against 17.6 of bytes: 12 us pass before the
+// sequence of 100k keys takes 42 us against 17.6 of bytes: 9 us pass before the
 // first and after the last tile, and seven or eight tiles a warp follow.
 #include <atomic>
 
@@ -168,6 +168,11 @@ __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
   return *reinterpret_cast<const uint32_t*>(&m);
 }
 
+// 2^e for e > -127; infinite above 127.
+__device__ __forceinline__ float power2(int e) {
+  return __uint_as_float((unsigned)min(e + 127, 255) << 23);
+}
+
 __device__ __forceinline__ int tiles_of(int t, long long cap) {
   return t >= 0 && t < cap ? t / kTileKeys + 1 : 0;
 }
@@ -256,7 +261,29 @@ __global__ void __launch_bounds__(kDecodeThreads, kCtasPerSm) decode_kernel(
   const int G = Hq / pg.Hkv, per_seq = pg.Hkv * n_hg;
   const int tpb = pg.block_rows / kTileKeys;
   const long long cap = (long long)pg.max_blocks * pg.block_rows;
-  const long long all = spans_before(t, B, cap, sums) * per_seq;
+  if (tid == 0) {
+    *abort_flag = 0;
+    bad_pages[0] = bad_pages[1] = 0;
+    for (int i = 0; i < kWarps * kRing; ++i) mbar_init(smem_u32(bars) + 8 * i, 1);
+    fence_barrier_init();
+  }
+  for (int i = tid; i < SM::kQ / 16; i += kDecodeThreads)  // heads a unit does not have
+    reinterpret_cast<uint4*>(qf)[i] = make_uint4(0, 0, 0, 0);
+  for (int i = tid; i < 3 * kHeads * kGr + kHeads; i += kDecodeThreads) qsum[i] = 0.f;
+  // spans of 32 sequences, and those of the ones up to the lane's
+  long long mine, sum;
+  auto scan = [&](int first) {
+    mine = first + lane < B ? (long long)span_of(__ldg(t + first + lane), cap) * per_seq : 0;
+    sum = mine;
+#pragma unroll
+    for (int sh = 1; sh < 32; sh <<= 1) {
+      const long long y = __shfl_up_sync(0xFFFFFFFFu, sum, sh);
+      if (lane >= sh) sum += y;
+    }
+  };
+  scan(0);
+  const long long all = B <= 32 ? __shfl_sync(0xFFFFFFFFu, sum, 31)
+                                : spans_before(t, B, cap, sums) * per_seq;
   const Split split = make_split(all, share_count(all, gridDim.x));
   if (blockIdx.x == 0) {  // positions outside the cache: reported, no work
     for (int b = tid; b < B; b += kDecodeThreads)
@@ -266,18 +293,10 @@ __global__ void __launch_bounds__(kDecodeThreads, kCtasPerSm) decode_kernel(
   long long at = share_begin(split, blockIdx.x);
   const long long end = share_begin(split, blockIdx.x + 1);
   // the sequence at the share's begin, and where that sequence begins (every
-  // warp looks, 32 sequences at a time)
+  // warp looks)
   int b = 0;
   long long b_at = 0;
-  for (;; b += 32) {
-    const long long mine =
-        b + lane < B ? (long long)span_of(__ldg(t + b + lane), cap) * per_seq : 0;
-    long long sum = mine;
-#pragma unroll
-    for (int sh = 1; sh < 32; sh <<= 1) {
-      const long long y = __shfl_up_sync(0xFFFFFFFFu, sum, sh);
-      if (lane >= sh) sum += y;
-    }
+  for (;;) {
     const unsigned past = __ballot_sync(0xFFFFFFFFu, at < b_at + sum);
     if (past) {
       const int k = __ffs(past) - 1;
@@ -286,22 +305,15 @@ __global__ void __launch_bounds__(kDecodeThreads, kCtasPerSm) decode_kernel(
       break;
     }
     b_at += __shfl_sync(0xFFFFFFFFu, sum, 31);
-  }
-  if (tid == 0) {
-    *abort_flag = 0;
-    for (int i = 0; i < kWarps * kRing; ++i) mbar_init(smem_u32(bars) + 8 * i, 1);
-    fence_barrier_init();
+    b += 32;
+    scan(b);
   }
   // This warp's ring: the K and V parts of its tiles pass in turn through its
   // buffers; a part is fetched as soon as the one kRing before it is read.
   const uint8_t* ring = smem + warp * kRing * SM::kHalf;
   const uint32_t full0 = smem_u32(bars) + warp * kRing * 8;
   int buf = 0, phase = 0;
-  if (tid == 0) bad_pages[0] = bad_pages[1] = 0;
-  for (int i = tid; i < SM::kQ / 16; i += kDecodeThreads)  // heads a unit does not have
-    reinterpret_cast<uint4*>(qf)[i] = make_uint4(0, 0, 0, 0);
-  for (int i = tid; i < 3 * kHeads * kGr + kHeads; i += kDecodeThreads) qsum[i] = 0.f;
-  int turned = -1;  // the sequence and DCA pieces whose rotations cs holds
+  int turned = -1, turns = 0;  // the sequence whose rotations cs holds, and for which DCA pieces
 
   for (int piece = 0; at < end; ++piece) {
   volatile int* bad_page = bad_pages + (piece & 1);
@@ -337,17 +349,20 @@ __global__ void __launch_bounds__(kDecodeThreads, kCtasPerSm) decode_kernel(
   uint4 q8 = {};
   if (has_q)
     q8 = __ldg(reinterpret_cast<const uint4*>(q + ((size_t)seq * Hq + h_base) * D) + tid);
-  const int turn = (seq * 3 + p_lo) * 3 + p_hi;
-  if (turned != turn) {
+  if (turned != seq) turns = 0;
+  turned = seq;
+  const int missing = ((2 << p_hi) - (1 << p_lo)) & ~turns;
+  if (missing) {
     const int im = tb % s;
 #pragma unroll 1
-    for (int x = p_lo * (D / 2) + tid; x < (p_hi + 1) * (D / 2); x += kDecodeThreads) {
+    for (int x = tid; x < 3 * (D / 2); x += kDecodeThreads) {
       const int p = x / (D / 2), k = x % (D / 2);
+      if (!(missing >> p & 1)) continue;
       double cd, sd;
       sincos64((double)query_pos_for_piece(p, im, s, c) * theta.v[k], cd, sd);
       cs[x] = make_float2((float)cd, (float)sd);
     }
-    turned = turn;
+    turns |= missing;
   }
   for (int i = tid; i < n_tiles; i += kDecodeThreads) {
     const int tile = tile0 + i;
@@ -391,7 +406,7 @@ __global__ void __launch_bounds__(kDecodeThreads, kCtasPerSm) decode_kernel(
       for (int sh = 16; sh >= 1; sh >>= 1) big = fmaxf(big, __shfl_xor_sync(~0u, big, sh));
       // every rotated value times 2^-e stays below 2^11
       const int e = big > 0.f ? (int)(__float_as_uint(big) >> 23) - 127 - 10 : 0;
-      const float down = ldexpf(1.f, -(e / 2)), down2 = ldexpf(1.f, -(e - e / 2));
+      const float down = power2(-(e / 2)), down2 = power2(-(e - e / 2));
       {
         float sum[2] = {0.f, 0.f};
 #pragma unroll
@@ -422,7 +437,7 @@ __global__ void __launch_bounds__(kDecodeThreads, kCtasPerSm) decode_kernel(
         const float unit = down * down2 * 5.9604644775390625e-8f;  // 2^-24
         if (lane < kGr) qsum[(p * kHeads + hh) * kGr + lane] = (lane == 0 ? sum[0] : sum[1]) * unit;
       }
-      if (lane == 0 && p == p_lo) qexp[hh] = ldexpf(1.f, e + 24);
+      if (lane == 0 && p == p_lo) qexp[hh] = power2(e + 24);
     }
     __syncthreads();
   }
