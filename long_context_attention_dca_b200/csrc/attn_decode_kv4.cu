@@ -30,14 +30,13 @@
 // capacity.  Kernel 2 merges the shares.
 //
 // What bounds it.  A key costs 144 bytes of cache a kv head (D = 128) and, with
-// eight query heads on it, about 17 instructions a warp (1100 for 64 keys, 96 of
+// eight query heads on it, about 18 instructions a warp (1145 for 64 keys, 96 of
 // them matrix products, half of the rest unpacking nibbles).  With one query
 // head memory bounds it: 24 sequences of 16k keys, 32 kv heads, take 290 us,
 // 6.1 TB/s, 93 % of the copy rate.  With eight, the instructions do: 16 sequences
 // of 33k to 65k keys, 8 kv heads, take 204 us, 4.4 TB/s, where the loads alone
-// take 143; the logic pipe is busy for half of it and the matrix pipe for 38 %, the
-// rest is fixed latency between them.  One
-// sequence of 100k keys takes 42 us against 17.6 of bytes: 9 us pass before the
+// take 143; the logic pipe is busy for half of it and the matrix pipe for 37 %, the
+// rest is fixed latency between them.  One sequence of 100k keys takes 42 us against 17.6 of bytes: 9 us pass before the
 // first and after the last tile, and seven or eight tiles a warp follow.
 #include <atomic>
 
