@@ -150,7 +150,9 @@ dca_status_t check_pages(const char* fn, const int* block_table, const int* refs
     const long long part = (long long)(block_rows / p.unit_rows) * (long long)p.unit_bytes;
     if (part > (1ll << 40) || p.outer > (1 << 20) || (part >> 12) * p.outer > (1ll << 30))
       return fail(DCA_ERR_UNSUPPORTED, "%s: pool %d: a page of over 2^42 bytes", fn, j);
-    items += (part >> 12) * p.outer;
+    items += ((part >> 14) + 1) * p.outer;
+    if (items > (1ll << 30))
+      return fail(DCA_ERR_UNSUPPORTED, "%s: a page of over 2^44 bytes in all pools", fn);
     list.p[j] = PoolDesc{static_cast<unsigned char*>(p.base), (long long)p.unit_bytes, p.outer,
                          p.unit_rows, 0, 0};
   }

@@ -38,9 +38,49 @@ template <int C>
 __device__ __forceinline__ int get(const int* p) {
   return C == 1 ? *p : __ldcg(p);
 }
-__device__ __forceinline__ int pages_of(int n, int R) {
-  return (int)(((long long)n + R - 1) / R);
+__device__ __forceinline__ int pages_of(int n, int R) {  // n >= 0, R <= 2^30
+  return (int)(((unsigned)n + (unsigned)R - 1u) / (unsigned)R);
 }
+// The entries of the block table dealt to the threads, every step-th one to each,
+// as (slot, place in it): one division to begin with, none to go on.  Taken N at
+// a time, whose loads are in flight together; an entry past the end is the first
+// one, not live.  Two at a time in shared memory (191 pages: 5.5 us against 5.6
+// with four), four in global memory (271887 ints: 50 us against 52 with two).
+template <int C>
+constexpr int kBatchOf = C == 1 ? 2 : 4;
+struct Entries {
+  int b, i, e, B, max_blocks, step, slots, places;
+  __device__ Entries(int first, int step_, int B_, int max_blocks_)
+      : b(first / max_blocks_),
+        i(first % max_blocks_),
+        e(first),
+        B(B_),
+        max_blocks(max_blocks_),
+        step(step_),
+        slots(step_ / max_blocks_),
+        places(step_ % max_blocks_) {}
+};
+template <int N>
+struct Batch {
+  int b[N], i[N], e[N];
+  bool live[N];
+  __device__ __forceinline__ explicit Batch(Entries& at) {
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+      live[u] = at.b < at.B;
+      b[u] = live[u] ? at.b : 0;
+      i[u] = live[u] ? at.i : 0;
+      e[u] = live[u] ? at.e : 0;
+      at.e += at.step;
+      at.b += at.slots;
+      at.i += at.places;
+      if (at.i >= at.max_blocks) {
+        at.i -= at.max_blocks;
+        ++at.b;
+      }
+    }
+  }
+};
 
 // Exclusive prefix sum of one value a thread over the block; `total` gets the sum.
 __device__ __forceinline__ int block_scan(int v, int* warp_sums, int& total) {
@@ -91,7 +131,7 @@ struct Work {  // all int32
   int* owner;   // [num_blocks] slot that keeps a partial page; a page's new index
   int* list;    // [num_blocks] free pages or holes, ascending
   int* table;   // [B * max_blocks] the table as it came
-  int* slots;   // [6][B] see Slot
+  int* slots;   // [6][B] see slot()
 };
 constexpr int kHead = 64;
 
@@ -105,9 +145,9 @@ size_t work_ints(int B, int max_blocks, int num_blocks) {
   return list_ints(B, num_blocks) + plan_ints(B, max_blocks, num_blocks);
 }
 // A plan of this many ints or fewer runs in one CTA's shared memory (200 KB).
-// Alone against a cluster in global memory, us (remap / compact): 1037 ints 5.4 /
-// 4.5 against 14.8 / 10.7, 16017 ints 13.8 / 10.8 against 18.9 / 13.8, 38073 ints
-// 20.3 / 15.2 against 23.3 / 16.1.
+// Alone against a cluster in global memory, us (remap / compact): 1037 ints 5.5 /
+// 5.0 against 15.7 / 11.2, 16017 ints 10.3 / 9.2 against 18.6 / 13.2, 38073 ints
+// 17.6 / 15.5 against 20.7 / 14.7.
 constexpr size_t kAloneInts = 50000;
 
 __host__ __device__ inline void carve_plan(Work& w, int* p, int B, int max_blocks,
@@ -130,35 +170,39 @@ Work carve(void* ws, int B, int max_blocks, int num_blocks) {
   return w;
 }
 
-// What becomes of a slot: keep = min(old_len[src], new_len) rows of old slot src
-// (none for -1), in whole pages and rows of a partial one.  Worked out once, by
-// a thread each, so that the phases find everything beside the table.
-struct Slot {
-  int src, full, rest;
-  int pages;  // of the new length
-  int used;   // of the old length
-};  // and, sixth, where its new pages start in the list
-template <int C>
-__device__ __forceinline__ Slot slot_at(const Work& w, int B, int b) {
-  Slot s;
-  s.src = get<C>(w.slots + b);
-  s.full = get<C>(w.slots + B + b);
-  s.rest = get<C>(w.slots + 2 * (size_t)B + b);
-  s.pages = get<C>(w.slots + 3 * (size_t)B + b);
-  s.used = get<C>(w.slots + 4 * (size_t)B + b);
-  return s;
+// What becomes of a slot, worked out once, by a thread each: keep = min(old_len[src],
+// new_len) rows of old slot src (none for -1) are `full` whole pages and `rest`
+// rows of the next.  Six arrays of the slots:
+enum {
+  kSrc,
+  kFull,
+  kRest,   // later 0 where the slot keeps the partial page itself: nothing to copy
+  kPages,  // of the new length
+  kUsed,   // of the old length; later the entries that stay, full pages and partial one
+  kFresh,  // entry i beyond those is the new page list[kFresh + i]
+};
+__device__ __forceinline__ int* slot(const Work& w, int what, int B, int b) {
+  return w.slots + (size_t)what * B + b;
 }
-// The table as it came into the working copy: independent loads, several in
-// flight a thread, since nothing else hides their latency.
-__device__ __forceinline__ void stage(const int* from, int* to, long long n, long long first,
-                                      int step) {
-#pragma unroll 8
-  for (long long e = first; e < n; e += step) to[e] = from[e];
+// The table as it came into the working copy: independent loads, eight in flight
+// a thread, since nothing else hides their latency.
+__device__ __forceinline__ void stage(const int* from, int* to, int n, int first, int step) {
+  for (long long e = first; e < n; e += 8ll * step) {
+    int v[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      v[u] = e + (long long)u * step < n ? from[e + (long long)u * step] : 0;
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (e + (long long)u * step < n) to[e + (long long)u * step] = v[u];
+  }
 }
 
 // Full pages are shared.  A partial last page goes to the lowest slot that wants
 // it unless it is still held elsewhere; every other slot gets a copy of its rows.
-// A warp walks a slot's entries.
+// The entries of the table are dealt to the threads one by one, whatever their
+// slots: 192 slots of 35 entries and 2715 pages take 10.3 us, against 13.7 with a
+// warp a slot; 2000 slots of 60 and 46629 pages 50 against 57.
 template <int C>
 __global__ void __cluster_dims__(C, 1, 1) __launch_bounds__(kPlanThreads, 1) remap_plan(
     const int* __restrict__ src, const int* __restrict__ old_len,
@@ -167,45 +211,55 @@ __global__ void __cluster_dims__(C, 1, 1) __launch_bounds__(kPlanThreads, 1) rem
     Work w) {
   __shared__ int sums[32];
   __shared__ int carry;
-  const int rank = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
-  const int gid = rank * kPlanThreads + tid, gwarp = gid >> 5;
-  constexpr int kAll = C * kPlanThreads, kWarps = kAll / 32;
+  const int rank = blockIdx.x, tid = threadIdx.x;
+  const int gid = rank * kPlanThreads + tid;
+  constexpr int kAll = C * kPlanThreads, kBatch = kBatchOf<C>;
+  const Entries first(gid, kAll, B, max_blocks);
   extern __shared__ int plan_smem[];
   if (C == 1) carve_plan(w, plan_smem, B, max_blocks, num_blocks);
   cudaTriggerProgrammaticLaunchCompletion();  // the copies may take their places
   const long long cap = (long long)max_blocks * R;
   if (rank == 0 && tid < kHead) w.head[tid] = 0;
   bool bad = false;
+  int f = 0, n = 0, o = 0;  // of the thread's first slot, fetched beside the table
+  if (gid < B) f = src[gid], n = new_len[gid], o = old_len[gid];
+  stage(table_in, w.table, B * max_blocks, gid, kAll);
+#pragma unroll 4
+  for (int p = gid; p < num_blocks; p += kAll) {
+    const int held = refs_in[p];
+    w.count[p] = held;
+    w.owner[p] = kNone;
+    bad |= held < 0;
+  }
   for (int b = gid; b < B; b += kAll) {
-    const int f = src[b], n = new_len[b], o = old_len[b];
+    if (b != gid) f = src[b], n = new_len[b], o = old_len[b];
     const bool fits = o >= 0 && o <= cap;
     bad |= f < -1 || f >= B || n < 0 || n > cap || !fits;
     const int keep = f < 0 || f >= B ? 0 : max(0, min(old_len[f], n));
-    w.slots[b] = f;
-    w.slots[B + b] = keep / R;
-    w.slots[2 * (size_t)B + b] = keep % R;
-    w.slots[3 * (size_t)B + b] = pages_of(max(n, 0), R);
-    w.slots[4 * (size_t)B + b] = fits ? pages_of(o, R) : 0;
-  }
-  stage(table_in, w.table, (long long)B * max_blocks, gid, kAll);
-#pragma unroll 4
-  for (int p = gid; p < num_blocks; p += kAll) {
-    const int n = refs_in[p];
-    w.count[p] = n;
-    w.owner[p] = kNone;
-    bad |= n < 0;
+    const int full = (int)((unsigned)keep / (unsigned)R);
+    *slot(w, kSrc, B, b) = f;
+    *slot(w, kFull, B, b) = full;
+    *slot(w, kRest, B, b) = keep - full * R;
+    *slot(w, kPages, B, b) = pages_of(max(n, 0), R);
+    *slot(w, kUsed, B, b) = fits ? pages_of(o, R) : 0;
   }
   phase_end<C>();
 
   // what the slots hold dropped from the counts; a fault anywhere refuses the
   // whole call
-  for (int b = gwarp; b < B; b += kWarps) {
-    const int used = get<C>(w.slots + 4 * (size_t)B + b);
-    const int* row = w.table + (size_t)b * max_blocks;
-    for (int i = lane; i < used; i += 32) {
-      const int p = get<C>(row + i);
-      if (p < 0 || p >= num_blocks) bad = true;
-      else if (atomicSub(w.count + p, 1) <= 0) bad = true;  // fewer than name it
+  for (Entries at = first; at.b < B;) {
+    const Batch<kBatch> x(at);
+    int p[kBatch], used[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      used[u] = get<C>(slot(w, kUsed, B, x.b[u]));
+      p[u] = get<C>(w.table + x.e[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      if (!x.live[u] || x.i[u] >= used[u]) continue;
+      if (p[u] < 0 || p[u] >= num_blocks) bad = true;
+      else if (atomicSub(w.count + p[u], 1) <= 0) bad = true;  // fewer than name it
     }
   }
   if (bad) atomicExch(w.head, 1);
@@ -214,19 +268,31 @@ __global__ void __cluster_dims__(C, 1, 1) __launch_bounds__(kPlanThreads, 1) rem
 
   // full pages are shared by every slot that keeps them
   if (!fault) {
-    for (int b = gwarp; b < B; b += kWarps) {
-      const Slot s = slot_at<C>(w, B, b);
-      const int* row = w.table + (size_t)max(s.src, 0) * max_blocks;
-      for (int i = lane; i < s.full; i += 32) atomicAdd(w.count + get<C>(row + i), 1);
+    for (Entries at = first; at.b < B;) {
+      const Batch<kBatch> x(at);
+      int p[kBatch], full[kBatch];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        full[u] = get<C>(slot(w, kFull, B, x.b[u]));
+        p[u] = max(get<C>(slot(w, kSrc, B, x.b[u])), 0) * max_blocks + x.i[u];
+      }
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) p[u] = get<C>(w.table + p[u]);
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u)
+        if (x.live[u] && x.i[u] < full[u]) atomicAdd(w.count + p[u], 1);
     }
   }
   phase_end<C>();
   // partial pages that nobody holds any more go to the lowest slot
+  auto tail_of = [&](int b) {
+    return get<C>(w.table + (size_t)get<C>(slot(w, kSrc, B, b)) * max_blocks +
+                  get<C>(slot(w, kFull, B, b)));
+  };
   if (!fault) {
     for (int b = gid; b < B; b += kAll) {
-      const Slot s = slot_at<C>(w, B, b);
-      if (s.rest == 0) continue;
-      const int p = get<C>(w.table + (size_t)s.src * max_blocks + s.full);
+      if (get<C>(slot(w, kRest, B, b)) == 0) continue;
+      const int p = tail_of(b);
       if (get<C>(w.count + p) == 0) atomicMin(w.owner + p, b);
     }
   }
@@ -248,19 +314,21 @@ __global__ void __cluster_dims__(C, 1, 1) __launch_bounds__(kPlanThreads, 1) rem
     __syncthreads();
     for (int b0 = 0; b0 < B; b0 += kPlanThreads) {
       const int b = b0 + tid;
-      int need = 0;
+      int need = 0, stay = 0;
       if (b < B && !fault) {
-        const Slot s = slot_at<C>(w, B, b);
-        int stays = 0;
-        if (s.rest) {
-          const int p = get<C>(w.table + (size_t)s.src * max_blocks + s.full);
-          stays = get<C>(w.owner + p) == b;
+        stay = get<C>(slot(w, kFull, B, b));
+        if (get<C>(slot(w, kRest, B, b)) && get<C>(w.owner + tail_of(b)) == b) {
+          ++stay;
+          *slot(w, kRest, B, b) = 0;
         }
-        need = s.pages - s.full - stays;
+        need = get<C>(slot(w, kPages, B, b)) - stay;
       }
       int total;
       const int before = block_scan(need, sums, total);
-      if (b < B) w.slots[5 * (size_t)B + b] = carry + before;
+      if (b < B) {
+        *slot(w, kUsed, B, b) = stay;
+        *slot(w, kFresh, B, b) = carry + before - stay;
+      }
       __syncthreads();
       if (tid == 0) carry += total;
       __syncthreads();
@@ -315,22 +383,32 @@ __global__ void __cluster_dims__(C, 1, 1) __launch_bounds__(kPlanThreads, 1) rem
   }
   phase_end<C>();
 
+  for (int b = gid; b < B; b += kAll) {
+    const int rest = get<C>(slot(w, kRest, B, b));
+    if (rest == 0) continue;
+    const int k = atomicAdd(w.head + 1, 1), full = get<C>(slot(w, kFull, B, b));
+    w.from[k] = tail_of(b);
+    w.to[k] = get<C>(w.list + get<C>(slot(w, kFresh, B, b)) + full);
+    w.rows[k] = rest;
+  }
   for (int p = gid; p < num_blocks; p += kAll) refs_out[p] = get<C>(w.count + p);
-  for (int b = gwarp; b < B; b += kWarps) {
-    const Slot s = slot_at<C>(w, B, b);
-    const int* row = w.table + (size_t)max(s.src, 0) * max_blocks;
-    const int tail = s.rest ? get<C>(row + s.full) : -1;
-    const int stays = s.rest && get<C>(w.owner + tail) == b;
-    const int* fresh = w.list + get<C>(w.slots + 5 * (size_t)B + b) - s.full - stays;
-    int* out = table_out + (size_t)b * max_blocks;
-    for (int i = lane; i < max_blocks; i += 32)
-      out[i] = i >= s.pages ? -1 : i < s.full + stays ? get<C>(row + i) : get<C>(fresh + i);
-    if (lane == 0 && s.rest && !stays) {
-      const int k = atomicAdd(w.head + 1, 1);
-      w.from[k] = tail;
-      w.to[k] = get<C>(fresh + s.full);
-      w.rows[k] = s.rest;
+  for (Entries at = first; at.b < B;) {
+    const Batch<kBatch> x(at);
+    const int* from[kBatch];
+    int page[kBatch], pages[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int b = x.b[u], i = x.i[u];
+      pages[u] = get<C>(slot(w, kPages, B, b));
+      const int src = get<C>(slot(w, kSrc, B, b)), fresh = get<C>(slot(w, kFresh, B, b));
+      from[u] = i < get<C>(slot(w, kUsed, B, b)) ? w.table + src * max_blocks + i
+                                                 : w.list + (i < pages[u] ? fresh + i : 0);
     }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) page[u] = get<C>(from[u]);
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u)
+      if (x.live[u]) table_out[x.e[u]] = x.i[u] < pages[u] ? page[u] : -1;
   }
   phase_end<C>();
   if (gid == 0) {
@@ -347,9 +425,10 @@ __global__ void __cluster_dims__(C, 1, 1) __launch_bounds__(kPlanThreads, 1) com
     int* refs_out, int* __restrict__ moved, int* __restrict__ info, int B, int max_blocks,
     int num_blocks, int R, Work w) {
   __shared__ int sums[32];
-  const int rank = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
-  const int gid = rank * kPlanThreads + tid, gwarp = gid >> 5;
-  constexpr int kAll = C * kPlanThreads, kWarps = kAll / 32;
+  const int rank = blockIdx.x, tid = threadIdx.x;
+  const int gid = rank * kPlanThreads + tid;
+  constexpr int kAll = C * kPlanThreads, kBatch = kBatchOf<C>;
+  const Entries first(gid, kAll, B, max_blocks);
   extern __shared__ int plan_smem[];
   if (C == 1) carve_plan(w, plan_smem, B, max_blocks, num_blocks);
   cudaTriggerProgrammaticLaunchCompletion();  // the copies may take their places
@@ -364,7 +443,7 @@ __global__ void __cluster_dims__(C, 1, 1) __launch_bounds__(kPlanThreads, 1) com
     bad |= !fits;
     w.slots[b] = fits ? pages_of(n, R) : 0;
   }
-  stage(table_in, w.table, (long long)B * max_blocks, gid, kAll);
+  stage(table_in, w.table, B * max_blocks, gid, kAll);
 #pragma unroll 4
   for (int p = mine.begin + tid; p < mine.end; p += kPlanThreads) {
     const int n = refs_in[p];
@@ -376,13 +455,19 @@ __global__ void __cluster_dims__(C, 1, 1) __launch_bounds__(kPlanThreads, 1) com
   block_scan(local, sums, part_live);
   if (tid == 0) w.head[8 + rank] = part_live;
   phase_end<C>();
-  for (int b = gwarp; b < B; b += kWarps) {
-    const int used = get<C>(w.slots + b);
-    const int* row = w.table + (size_t)b * max_blocks;
-    for (int i = lane; i < used; i += 32) {
-      const int p = get<C>(row + i);
-      if (p < 0 || p >= num_blocks || get<C>(w.count + p) <= 0) bad = true;
-    }
+  for (Entries at = first; at.b < B;) {
+    const Batch<kBatch> x(at);
+    int p[kBatch], n[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u)
+      p[u] = x.live[u] && x.i[u] < get<C>(w.slots + x.b[u]) ? get<C>(w.table + x.e[u]) : kNone;
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u)
+      n[u] = get<C>(w.count + ((unsigned)p[u] < (unsigned)num_blocks ? p[u] : 0));
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u)
+      bad |= x.live[u] && x.i[u] < get<C>(w.slots + x.b[u]) &&
+             ((unsigned)p[u] >= (unsigned)num_blocks || n[u] <= 0);
   }
   if (bad) atomicExch(w.head, 1);
   int before = 0, live = 0;
@@ -439,11 +524,20 @@ __global__ void __cluster_dims__(C, 1, 1) __launch_bounds__(kPlanThreads, 1) com
     w.rows[k] = R;
   }
   phase_end<C>();
-  for (int b = gwarp; b < B; b += kWarps) {
-    const int used = get<C>(w.slots + b);
-    const size_t row = (size_t)b * max_blocks;
-    for (int i = lane; i < max_blocks; i += 32)
-      table_out[row + i] = i < used ? get<C>(w.owner + get<C>(w.table + row + i)) : -1;
+  for (Entries at = first; at.b < B;) {
+    const Batch<kBatch> x(at);
+    int p[kBatch];
+    bool used[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      used[u] = x.i[u] < get<C>(w.slots + x.b[u]);
+      p[u] = get<C>(w.table + x.e[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) p[u] = get<C>(w.owner + (used[u] ? p[u] : 0));
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u)
+      if (x.live[u]) table_out[x.e[u]] = used[u] ? p[u] : -1;
   }
   if (gid == 0) {
     info[0] = live;

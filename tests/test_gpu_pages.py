@@ -110,6 +110,22 @@ def test_remap_many_slots_and_pages():
     assert got == tuple(want[:3])
 
 
+@pytest.mark.parametrize("B,most", [(2, 9500), (1, 1), (5000, 1), (3, 1024), (9, 1023), (5, 4097),
+                                    (1, 30000), (40, 1025)])
+def test_long_rows_and_many_short_ones(B, most):
+    # rows as long as, longer and shorter than the threads that share the entries
+    rng = np.random.default_rng(B)
+    lens, table, refs, num = ku.random_slots(rng, B, most, 1, extra=most + 3 * B, pins=5)
+    src = [int(x) for x in rng.integers(-1, B, B)]
+    new = [int(rng.integers(0, most + 1)) for _ in range(B)]
+    want = ko.remap(src, lens, new, table, refs, 1)
+    assert _remap(src, lens, new, table, refs, [], 1) == tuple(want[:3])
+    want = ko.compact(lens, table, refs, 1)
+    got = dca.dca_pages_compact(ku.ints(lens), ku.ints(table), ku.ints(refs), [], 1)
+    assert tuple(x.tolist() for x in got) == tuple(want[:4])
+    dca.dca_sync_status()
+
+
 def test_remap_with_missing_pages_changes_nothing():
     lens, table = [70, 64], [[2, 0, -1], [1, -1, -1]]
     pools = _pools(4, 64, 5)

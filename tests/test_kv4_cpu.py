@@ -292,6 +292,14 @@ def test_page_refusals(lib, call, want, args):
     assert call(lib, **args) == want
 
 
+@pytest.mark.parametrize("call", [_remap, _compact])
+def test_page_pools_too_large_together(lib, call):
+    # each page is 2^40 bytes, which one pool may have; 256 of them are more than
+    # the copies can number
+    pools = (dca._PagePool * 256)(*[(0x30000, 1 << 20, 1 << 20, 64)] * 256)
+    assert call(lib, n=256, pools=ctypes.byref(pools)) == 2
+
+
 @pytest.mark.parametrize("call,args", [(_remap, dict(src=None)), (_remap, dict(old=None)),
                                        (_remap, dict(new=P(0x10001))),
                                        (_compact, dict(lens=None)), (_compact, dict(moved=None))])
