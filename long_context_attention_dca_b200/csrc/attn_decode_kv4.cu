@@ -55,7 +55,6 @@ constexpr int kHeads = 8;   // query heads per CTA (MMA N)
 // 47 and 212, one of twelve 87, 48 and 235.
 constexpr int kWarps = 4;
 constexpr int kRing = 3;
-constexpr int kDecodeThreads = kWarps * 32;
 constexpr int kCtasPerSm = 3;
 constexpr int kMany = 2;    // 16-key steps whose score products run interleaved: 208 us with one
                             // for the last of those, 204 with two
@@ -72,6 +71,19 @@ constexpr int kMaxTiles = 512;  // of a CTA's share, so that their places fit in
 // 40 sequences of 1k to 30k keys, a setup of 6, 8, 9, 10 and 12 tiles differed by
 // at most 1.4 % in the mean, 8 the fastest.
 constexpr int kSetup = 8;
+// Where the caches are short, a unit is not cut: a CTA takes it whole, writes its
+// outputs, and there is nothing to merge.  Against equal shares, in a graph: 64 to
+// 148 units of 100 / 500 / 1000 / 2000 keys, 8 query heads, 9.1 / 9.5 / 12.0 / 16.9
+// us against 12.8 / 16.9 / 19.6 / 22.8; 512 units 20.5 / 24.7 / 33.5 / 52.5 against
+// 22.3 / 28.3 / 37.8 / 54.5, and slower from 3000 keys on; 8 units 8.7 / 9.2 / 11.6 /
+// 16.4 against 10.5 / 10.9 / 10.2 / 10.4, where one launch fewer also saves 4 us
+// of the host's time, which is what such a call waits for outside a graph.
+constexpr int kWide = 8;  // warps of such a CTA where every unit has an SM to itself: 1000 keys
+                          // take 12.0 us, 13.8 with twelve, 14.6 with four
+constexpr long long kWholeUnits = 1 << 20;  // the launch grid
+inline bool takes_whole(long long units, long long cap) {  // cap: rows of a cache
+  return units <= kWholeUnits && cap <= (units < 64 ? 1024 : 2048);
+}
 struct Split {
   long long shares, each, extra;  // the first `extra` shares hold one tile more
 };
@@ -108,20 +120,20 @@ inline long long decode_shares(int B, int Hq, int Hkv, long long cap) {
   return share_count(tiles, need > 148 * kCtasPerSm ? need : 148 * kCtasPerSm);
 }
 
-template <int D>
+template <int D, int W>
 struct DecodeSmem {
   static constexpr int kHalf = Tile<D>::kBytes / 2;
-  static constexpr int kRings = kWarps * kRing * kHalf;
+  static constexpr int kRings = W * kRing * kHalf;
   // [piece][hi, lo][group][head][word] x 16 bytes of query fragments
   static constexpr int kQ = 3 * 2 * (D / 64) * kHeads * 8 * 16;
   static constexpr int kCs = 3 * (D / 2) * 8;          // cos, sin
   static constexpr int kRaw = kHeads * D * 2;          // queries as they came
   static constexpr int kSums = 3 * kHeads * (D / 64) * 4;  // sum of q per group
   static constexpr int kF = kHeads * 4;
-  static constexpr int kBars = kWarps * kRing * 8 + 16;  // + abort and page words
+  static constexpr int kBars = W * kRing * 8 + 16;  // + abort and page words
   static constexpr int kPlaces = kMaxTiles * 4;  // pool tile of every tile of the share
   static constexpr int kTotal = kRings + kQ + kRaw + kCs + kSums + kF + kBars + kPlaces;
-  static_assert(kWarps * kHeads * (D + 2) * 4 <= kRings, "merge area");
+  static_assert(W * kHeads * (D + 2) * 4 <= kRings, "merge area");
 };
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
@@ -235,23 +247,25 @@ __device__ __forceinline__ void pv(float (&o)[D / 16][kOut], const uint32_t (&wg
 // kFew: at most four query heads a kv head.  Eight MMA columns then hold both
 // parts of every query, half the score products: 66 us for 24 x 4k keys of 32 kv
 // heads with a query head each, against 77 as eight columns of high parts.
-template <int D, bool kFew>
-__global__ void __launch_bounds__(kDecodeThreads, kCtasPerSm) decode_kernel(
+template <int D, bool kFew, int W>
+__global__ void __launch_bounds__(W * 32, W == kWarps ? kCtasPerSm : 1) decode_kernel(
     const __nv_bfloat16* __restrict__ q, Pages pg, const int* __restrict__ t,
-    float* __restrict__ Opart, float2* __restrict__ MLpart, int B, int Hq, int s, int c,
-    float scale_log2, int n_hg, const __grid_constant__ Theta theta) {
+    float* __restrict__ Opart, float2* __restrict__ MLpart, __nv_bfloat16* __restrict__ O,
+    float* __restrict__ LSE, int B, int Hq, int s, int c, float scale_log2, int n_hg,
+    bool whole_units, const __grid_constant__ Theta theta) {
   using TL = Tile<D>;
-  using SM = DecodeSmem<D>;
+  using SM = DecodeSmem<D, W>;
+  constexpr int kThreads = W * 32;
   constexpr int kGr = TL::kGroups, kOwn = kFew ? 1 : 2;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ long long sums[kWarps];
+  __shared__ long long sums[W];
   uint8_t* qf = smem + SM::kRings;
   __nv_bfloat16* qraw = reinterpret_cast<__nv_bfloat16*>(qf + SM::kQ);
   float2* cs = reinterpret_cast<float2*>(qf + SM::kQ + SM::kRaw);
   float* qsum = reinterpret_cast<float*>(qf + SM::kQ + SM::kRaw + SM::kCs);  // [piece][head][group]
   float* qexp = qsum + 3 * kHeads * kGr;                          // [head]
   uint8_t* bars = reinterpret_cast<uint8_t*>(qexp + kHeads);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + kWarps * kRing * 8);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + W * kRing * 8);
   volatile int* bad_pages = abort_flag + 1;  // [2], of this piece and of the next
   uint32_t* places = reinterpret_cast<uint32_t*>(bars + SM::kBars);
 
@@ -263,12 +277,12 @@ __global__ void __launch_bounds__(kDecodeThreads, kCtasPerSm) decode_kernel(
   if (tid == 0) {
     *abort_flag = 0;
     bad_pages[0] = bad_pages[1] = 0;
-    for (int i = 0; i < kWarps * kRing; ++i) mbar_init(smem_u32(bars) + 8 * i, 1);
+    for (int i = 0; i < W * kRing; ++i) mbar_init(smem_u32(bars) + 8 * i, 1);
     fence_barrier_init();
   }
-  for (int i = tid; i < SM::kQ / 16; i += kDecodeThreads)  // heads a unit does not have
+  for (int i = tid; i < SM::kQ / 16; i += kThreads)  // heads a unit does not have
     reinterpret_cast<uint4*>(qf)[i] = make_uint4(0, 0, 0, 0);
-  for (int i = tid; i < 3 * kHeads * kGr + kHeads; i += kDecodeThreads) qsum[i] = 0.f;
+  for (int i = tid; i < 3 * kHeads * kGr + kHeads; i += kThreads) qsum[i] = 0.f;
   // spans of 32 sequences, and those of the ones up to the lane's
   long long mine, sum;
   auto scan = [&](int first) {
@@ -280,32 +294,46 @@ __global__ void __launch_bounds__(kDecodeThreads, kCtasPerSm) decode_kernel(
       if (lane >= sh) sum += y;
     }
   };
-  scan(0);
-  const long long all = B <= 32 ? __shfl_sync(0xFFFFFFFFu, sum, 31)
-                                : spans_before(t, B, cap, sums) * per_seq;
-  const Split split = make_split(all, share_count(all, gridDim.x));
-  if (blockIdx.x == 0) {  // positions outside the cache: reported, no work
-    for (int b = tid; b < B; b += kDecodeThreads)
-      if (tiles_of(__ldg(t + b), cap) == 0) report_error(kDevBadArg, 207);
-  }
-  if (blockIdx.x >= split.shares || all == 0) return;
-  long long at = share_begin(split, blockIdx.x);
-  const long long end = share_begin(split, blockIdx.x + 1);
-  // the sequence at the share's begin, and where that sequence begins (every
-  // warp looks)
+  long long at, end, b_at = 0;  // the share, and where its first sequence begins
   int b = 0;
-  long long b_at = 0;
-  for (;;) {
-    const unsigned past = __ballot_sync(0xFFFFFFFFu, at < b_at + sum);
-    if (past) {
-      const int k = __ffs(past) - 1;
-      b_at += __shfl_sync(0xFFFFFFFFu, sum - mine, k);
-      b += k;
-      break;
+  if (whole_units) {
+    // a unit a CTA, as if its sequence were alone
+    b = blockIdx.x / per_seq;
+    const int u = blockIdx.x % per_seq, span = span_of(__ldg(t + b), cap);
+    at = (long long)u * span;
+    end = at + span;
+    if (span == 0) {  // a position outside the cache: reported, NaN
+      if (tid == 0 && u == 0) report_error(kDevBadArg, 207);
+      const int h0 = u / n_hg * G + u % n_hg * kHeads;
+      const int h1 = min(h0 + kHeads, u / n_hg * G + G);
+      for (int x = h0 * D + tid; x < h1 * D; x += kThreads)
+        O[(size_t)b * Hq * D + x] = __ushort_as_bfloat16(0x7FC0);
+      if (tid < h1 - h0) LSE[(size_t)b * Hq + h0 + tid] = __int_as_float(0x7fc00000);
     }
-    b_at += __shfl_sync(0xFFFFFFFFu, sum, 31);
-    b += 32;
-    scan(b);
+  } else {
+    scan(0);
+    const long long all = B <= 32 ? __shfl_sync(0xFFFFFFFFu, sum, 31)
+                                  : spans_before(t, B, cap, sums) * per_seq;
+    const Split split = make_split(all, share_count(all, gridDim.x));
+    if (blockIdx.x == 0) {  // positions outside the cache: reported, no work
+      for (int k = tid; k < B; k += kThreads)
+        if (tiles_of(__ldg(t + k), cap) == 0) report_error(kDevBadArg, 207);
+    }
+    if (blockIdx.x >= split.shares || all == 0) return;
+    at = share_begin(split, blockIdx.x);
+    end = share_begin(split, blockIdx.x + 1);
+    for (;;) {  // every warp looks for the sequence at the share's begin
+      const unsigned past = __ballot_sync(0xFFFFFFFFu, at < b_at + sum);
+      if (past) {
+        const int k = __ffs(past) - 1;
+        b_at += __shfl_sync(0xFFFFFFFFu, sum - mine, k);
+        b += k;
+        break;
+      }
+      b_at += __shfl_sync(0xFFFFFFFFu, sum, 31);
+      b += 32;
+      scan(b);
+    }
   }
   // This warp's ring: the K and V parts of its tiles pass in turn through its
   // buffers; a part is fetched as soon as the one kRing before it is read.
@@ -354,7 +382,7 @@ __global__ void __launch_bounds__(kDecodeThreads, kCtasPerSm) decode_kernel(
   if (missing) {
     const int im = tb % s;
 #pragma unroll 1
-    for (int x = tid; x < 3 * (D / 2); x += kDecodeThreads) {
+    for (int x = tid; x < 3 * (D / 2); x += kThreads) {
       const int p = x / (D / 2), k = x % (D / 2);
       if (!(missing >> p & 1)) continue;
       double cd, sd;
@@ -363,7 +391,7 @@ __global__ void __launch_bounds__(kDecodeThreads, kCtasPerSm) decode_kernel(
     }
     turns |= missing;
   }
-  for (int i = tid; i < n_tiles; i += kDecodeThreads) {
+  for (int i = tid; i < n_tiles; i += kThreads) {
     const int tile = tile0 + i;
     if (i != tid) blk = __ldg(pages + tile / tpb);
     if ((unsigned)blk >= (unsigned)pg.num_blocks) {
@@ -375,10 +403,10 @@ __global__ void __launch_bounds__(kDecodeThreads, kCtasPerSm) decode_kernel(
   }
   if (has_q) reinterpret_cast<uint4*>(qraw)[tid] = q8;
   __syncthreads();
-  const int parts = n_tiles > warp ? 2 * ((n_tiles - warp + kWarps - 1) / kWarps) : 0;
+  const int parts = n_tiles > warp ? 2 * ((n_tiles - warp + W - 1) / W) : 0;
   // lane 0: fetch part i of this warp's tiles into buffer `to`
   auto fetch = [&](int i, int to) {
-    const uint8_t* src = pg.pool + (size_t)places[warp + (i >> 1) * kWarps] * TL::kBytes +
+    const uint8_t* src = pg.pool + (size_t)places[warp + (i >> 1) * W] * TL::kBytes +
                          (i & 1) * SM::kHalf;
     const uint32_t bar = full0 + 8 * to;
     mbar_arrive_expect_tx(bar, SM::kHalf);
@@ -392,7 +420,7 @@ __global__ void __launch_bounds__(kDecodeThreads, kCtasPerSm) decode_kernel(
   {
     constexpr int kPairs = D / 64;  // (k, k + D/2) pairs a lane owns of a head
 #pragma unroll 1
-    for (int job = warp; job < (p_hi - p_lo + 1) * n_heads; job += kWarps) {
+    for (int job = warp; job < (p_hi - p_lo + 1) * n_heads; job += W) {
       const int p = p_lo + job / n_heads, hh = job % n_heads;  // a piece and a head
       float x0[kPairs], x1[kPairs], big = 0.f;
 #pragma unroll
@@ -480,7 +508,7 @@ __global__ void __launch_bounds__(kDecodeThreads, kCtasPerSm) decode_kernel(
       }
     };
 #pragma unroll 1
-    for (int it = warp; it < n_tiles; it += kWarps) {
+    for (int it = warp; it < n_tiles; it += W) {
       if (!warp_wait(full0 + 8 * buf, phase, abort_flag, 402)) break;
       const int j0 = (tile0 + it) * kTileKeys;
       const int j1 = min(j0 + kTileKeys - 1, tb);  // last valid key of the tile
@@ -721,8 +749,8 @@ __global__ void __launch_bounds__(kDecodeThreads, kCtasPerSm) decode_kernel(
   }
 
   float* mo = reinterpret_cast<float*>(smem);   // [warp][head][D]
-  float* mm = mo + kWarps * kHeads * D;         // [warp][head]
-  float* ml = mm + kWarps * kHeads;             // [warp][head]
+  float* mm = mo + W * kHeads * D;         // [warp][head]
+  float* ml = mm + W * kHeads;             // [warp][head]
   {
 #pragma unroll
     for (int gr = 0; gr < kGr; ++gr)
@@ -745,22 +773,28 @@ __global__ void __launch_bounds__(kDecodeThreads, kCtasPerSm) decode_kernel(
   }
   __syncthreads();
   const float poison = *bad_page ? __int_as_float(0x7fc00000) : 0.f;
-  for (int idx = tid; idx < n_heads * D; idx += kDecodeThreads) {
+  for (int idx = tid; idx < n_heads * D; idx += kThreads) {
     const int hh = idx / D, d = idx % D;
     float M = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, mm[w * kHeads + hh]);
+    for (int w = 0; w < W; ++w) M = fmaxf(M, mm[w * kHeads + hh]);
     const float mu = M == -INFINITY ? 0.f : M;
     float acc = poison, lsum = poison;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
+    for (int w = 0; w < W; ++w) {
       const float f = fast_exp2(mm[w * kHeads + hh] - mu);
       acc += f * mo[(w * kHeads + hh) * D + d];
       lsum += f * ml[w * kHeads + hh];
     }
-    const size_t slot = ((size_t)seq * per_seq + unit + blockIdx.x) * kHeads + hh;
-    Opart[slot * D + d] = acc;
-    if (d == 0) MLpart[slot] = make_float2(M, lsum);
+    if (whole_units) {
+      const size_t row = (size_t)seq * Hq + h_base + hh;
+      O[row * D + d] = __float2bfloat16_rn(acc / lsum);
+      if (d == 0) LSE[row] = (mu + log2f(lsum)) * 0.69314718055994530942f;
+    } else {
+      const size_t slot = ((size_t)seq * per_seq + unit + blockIdx.x) * kHeads + hh;
+      Opart[slot * D + d] = acc;
+      if (d == 0) MLpart[slot] = make_float2(M, lsum);
+    }
   }
   // the buffers go back to the copies of the next piece
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -848,7 +882,7 @@ __global__ void __launch_bounds__(kMergeThreads) decode_merge(
 }
 
 namespace {
-std::atomic<unsigned long long> g_smem_set[4];  // by kernel: a bit a device
+std::atomic<unsigned long long> g_smem_set[8];  // by kernel: a bit a device
 }
 
 template <int D>
@@ -861,11 +895,15 @@ cudaError_t launch_decode_t(const void* q, const Pages& pg, const int* t, void* 
   const size_t slots = ((size_t)B * pg.Hkv * n_hg + shares) * kHeads;
   float* Opart = static_cast<float*>(workspace);
   float2* MLpart = reinterpret_cast<float2*>(Opart + slots * D);
-  const bool few = Hq / pg.Hkv <= 4;
-  auto kern = few ? decode_kernel<D, true> : decode_kernel<D, false>;
-  constexpr int smem = DecodeSmem<D>::kTotal;
+  const long long units = (long long)B * pg.Hkv * n_hg;
+  const bool few = Hq / pg.Hkv <= 4, whole_units = takes_whole(units, cap);
+  const bool wide = whole_units && units <= 148;
+  auto kern = wide ? (few ? decode_kernel<D, true, kWide> : decode_kernel<D, false, kWide>)
+                   : (few ? decode_kernel<D, true, kWarps> : decode_kernel<D, false, kWarps>);
+  const int threads = (wide ? kWide : kWarps) * 32;
+  const int smem = wide ? DecodeSmem<D, kWide>::kTotal : DecodeSmem<D, kWarps>::kTotal;
   // once a device: the attribute stays with the function there
-  std::atomic<unsigned long long>& set = g_smem_set[D / 128 * 2 + few];
+  std::atomic<unsigned long long>& set = g_smem_set[D / 128 * 4 + wide * 2 + few];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess && (dev >= 64 || !(set.load() >> dev & 1))) {
@@ -873,15 +911,14 @@ cudaError_t launch_decode_t(const void* q, const Pages& pg, const int* t, void* 
     if (e == cudaSuccess && dev < 64) set.fetch_or(1ull << dev);
   }
   if (e != cudaSuccess) return e;
-  kern<<<shares, kDecodeThreads, smem, stream>>>(
-      static_cast<const __nv_bfloat16*>(q), pg, t, Opart, MLpart, B, Hq, s, c,
-      scale * 1.4426950408889634f, n_hg, make_theta(D, base));
+  kern<<<whole_units ? (int)units : shares, threads, smem, stream>>>(
+      static_cast<const __nv_bfloat16*>(q), pg, t, Opart, MLpart, static_cast<__nv_bfloat16*>(O),
+      LSE, B, Hq, s, c, scale * 1.4426950408889634f, n_hg, whole_units, make_theta(D, base));
   e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || whole_units) return e;
   // Warps by the partials a unit has on average.  With few, a warp a head: 62
   // sequences of 100 keys with 128 heads take 10 us, against 37 as 7936 blocks of
   // a head each.  With many, a block a head (one sequence of 100k keys, 64 heads).
-  const long long units = (long long)B * pg.Hkv * n_hg;
   auto merge = shares > 4 * units ? decode_merge<D, 1> : decode_merge<D, 8>;
   const int rows = shares > 4 * units ? 1 : 8;
   return launch_early(merge, dim3((Hq + rows - 1) / rows, B), kMergeThreads, stream,

@@ -223,8 +223,13 @@ def test_read_gives_the_stored_values_packed_and_as_a_cache(D):
     assert (short[3] == 7).all() and not (short[0, 60:65] == 7).all()
 
 
+def _with_room(table, rows, R):
+    """The table with room for that many more rows, named by no page."""
+    return np.pad(table, ((0, 0), (0, -(-rows // R))), constant_values=-1)
+
+
 def _decode_case(seed, D, Hq, Hkv, R, t, s, c, base=10000.0, scale=0.0, q=None, pool=None,
-                 table=None):
+                 table=None, rows=0):
     rng = np.random.default_rng(seed)
     gen = torch.Generator().manual_seed(seed)
     if table is None:
@@ -239,6 +244,7 @@ def _decode_case(seed, D, Hq, Hkv, R, t, s, c, base=10000.0, scale=0.0, q=None, 
                         ko.write_row(tile[h, r // 64], what, r % 64, np.full(D, 15, np.uint8),
                                      np.full(D // 64, np.nan), np.full(D // 64, np.nan))
     q = ku.bf16_rows(gen, len(t), Hq, D) if q is None else q
+    table = _with_room(table, rows, R)
     got = dca.dca_attn_decode_kv4_paged(q.cuda(), torch.from_numpy(pool).cuda(), ku.ints(table),
                                         ku.ints(t), s, c, base, scale)
     dca.dca_sync_status()
@@ -263,6 +269,19 @@ def _close(got, want, what=""):
 ])
 def test_decode_matches_the_oracle(D, Hq, Hkv, R, t, s, c):
     _close(*_decode_case(10, D, Hq, Hkv, R, t, s, c))
+
+
+@pytest.mark.parametrize("D,Hq,Hkv,R,t,s,c", [
+    (128, 1, 1, 64, [0], 4, 6), (64, 8, 1, 64, [1, 63, 64, 65], 100, 130),
+    (128, 16, 2, 128, [300, 0, 511, 127], 64, 100), (64, 20, 2, 64, [129], 7, 11),
+    (128, 3, 3, 256, [255, 256], 1, 1), (64, 5, 5, 64, [400], 333, 500),
+    (128, 24, 24, 64, [700, 9, 40], 256, 384), (64, 90, 30, 64, [1, 2, 63, 64, 2047, 900], 99, 120),
+    (128, 99, 33, 128, [2047, 5, 128, 0, 640], 500, 600),
+])
+def test_decode_of_short_sequences_in_caches_of_any_size(D, Hq, Hkv, R, t, s, c):
+    # a CTA a unit where the cache is short, shares where it has room for more
+    for rows in (0, 4096):
+        _close(*_decode_case(12, D, Hq, Hkv, R, t, s, c, rows=rows), rows)
 
 
 @pytest.mark.parametrize("D", [64, 128])
@@ -322,7 +341,8 @@ def test_decode_of_values_whose_scales_span_many_decades():
     _close(*_decode_case(18, D, 8, Hkv, R, t, 100, 150, table=table, pool=pool))
 
 
-def test_decode_reads_nan_rows_as_nan_and_only_there():
+@pytest.mark.parametrize("rows", [0, 4096])
+def test_decode_reads_nan_rows_as_nan_and_only_there(rows):
     rng = np.random.default_rng(19)
     D, Hkv, R, t = 128, 2, 64, [100, 100]
     table, num = ku.random_tables(rng, [101, 101], R)
@@ -333,8 +353,8 @@ def test_decode_reads_nan_rows_as_nan_and_only_there():
                  np.array([0.1, np.nan]), np.array([0.0, np.nan]))               # one value group
     gen = torch.Generator().manual_seed(19)
     q = ku.bf16_rows(gen, 2, 4, D)
-    O, LSE = dca.dca_attn_decode_kv4_paged(q.cuda(), torch.from_numpy(pool).cuda(), ku.ints(table),
-                                           ku.ints(t), 30, 40)
+    O, LSE = dca.dca_attn_decode_kv4_paged(q.cuda(), torch.from_numpy(pool).cuda(),
+                                           ku.ints(_with_room(table, rows, R)), ku.ints(t), 30, 40)
     dca.dca_sync_status()
     bad = torch.isnan(O.cpu())
     want = torch.zeros_like(bad)
@@ -345,7 +365,8 @@ def test_decode_reads_nan_rows_as_nan_and_only_there():
                                                             [False] * 4]))
 
 
-def test_decode_reports_bad_positions_and_pages():
+@pytest.mark.parametrize("rows", [0, 4096])
+def test_decode_reports_bad_positions_and_pages(rows):
     rng = np.random.default_rng(20)
     D, Hkv, R = 128, 2, 64
     table, num = ku.random_tables(rng, [128, 128, 128], R)
@@ -355,7 +376,7 @@ def test_decode_reports_bad_positions_and_pages():
     want = ko.decode(ku.f64(q), pool, table, [127, 127, 127], 30, 40)
     for t, entry in (([127, 128, 127], None), ([127, -1, 127], None), ([127, 127, 127], num),
                      ([127, 127, 127], -1)):
-        tab = table.copy()
+        tab = _with_room(table, rows, R)
         if entry is not None:
             tab[1, 1] = entry
         O, LSE = dca.dca_attn_decode_kv4_paged(q.cuda(), torch.from_numpy(pool).cuda(),
