@@ -27,17 +27,19 @@
 // bulk copy) through a small ring, so that the running maximum, its shuffles
 // and the update of O are paid once per 64 keys of a warp.  The sequence's
 // tiles are shared out evenly on the device from t[b], whatever the cache's
-// capacity.  Kernel 2 merges the shares.
+// capacity.  Kernel 2 merges the shares.  Where the caches are short a CTA takes a
+// unit whole and there is no second kernel.
 //
 // What bounds it.  A key costs 144 bytes of cache a kv head (D = 128) and, with
 // eight query heads on it, about 18 instructions a warp (1145 for 64 keys, 96 of
 // them matrix products, half of the rest unpacking nibbles).  With one query
-// head memory bounds it: 24 sequences of 16k keys, 32 kv heads, take 290 us,
-// 6.1 TB/s, 93 % of the copy rate.  With eight, the instructions do: 16 sequences
-// of 33k to 65k keys, 8 kv heads, take 204 us, 4.4 TB/s, where the loads alone
-// take 143; the logic pipe is busy for half of it and the matrix pipe for 37 %, the
-// rest is fixed latency between them.  One sequence of 100k keys takes 42 us against 17.6 of bytes: 9 us pass before the
-// first and after the last tile, and seven or eight tiles a warp follow.
+// head memory bounds it: 24 sequences of 16k keys, 32 kv heads, take 293 us,
+// 6.0 TB/s, 92 % of the copy rate.  With eight, the instructions do: 16 sequences
+// of 33k to 65k keys, 8 kv heads, take 205 us, 4.4 TB/s, where the loads alone
+// take 143; the logic pipe is busy for half of it and the matrix pipe for 37 %,
+// the rest is fixed latency between them.  One sequence of 100k keys takes 42 us
+// against 17.6 of bytes: 9 us pass before the first and after the last tile, and
+// seven or eight tiles a warp follow.
 #include <atomic>
 
 #include "dca_common.cuh"
@@ -148,7 +150,8 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 // gathers all loads of a tile first and spills.
 __device__ __forceinline__ void mma_codes(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                           uint32_t b1) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -247,12 +250,12 @@ __device__ __forceinline__ void pv(float (&o)[D / 16][kOut], const uint32_t (&wg
 // kFew: at most four query heads a kv head.  Eight MMA columns then hold both
 // parts of every query, half the score products: 66 us for 24 x 4k keys of 32 kv
 // heads with a query head each, against 77 as eight columns of high parts.
-template <int D, bool kFew, int W>
+template <int D, bool kFew, int W, bool kWhole>
 __global__ void __launch_bounds__(W * 32, W == kWarps ? kCtasPerSm : 1) decode_kernel(
     const __nv_bfloat16* __restrict__ q, Pages pg, const int* __restrict__ t,
     float* __restrict__ Opart, float2* __restrict__ MLpart, __nv_bfloat16* __restrict__ O,
     float* __restrict__ LSE, int B, int Hq, int s, int c, float scale_log2, int n_hg,
-    bool whole_units, const __grid_constant__ Theta theta) {
+    const __grid_constant__ Theta theta) {
   using TL = Tile<D>;
   using SM = DecodeSmem<D, W>;
   constexpr int kThreads = W * 32;
@@ -296,7 +299,7 @@ __global__ void __launch_bounds__(W * 32, W == kWarps ? kCtasPerSm : 1) decode_k
   };
   long long at, end, b_at = 0;  // the share, and where its first sequence begins
   int b = 0;
-  if (whole_units) {
+  if (kWhole) {
     // a unit a CTA, as if its sequence were alone
     b = blockIdx.x / per_seq;
     const int u = blockIdx.x % per_seq, span = span_of(__ldg(t + b), cap);
@@ -451,7 +454,8 @@ __global__ void __launch_bounds__(W * 32, W == kWarps ? kCtasPerSm : 1) decode_k
             const float z = y[v] * down * down2, whole = rintf(z), by = (n & 1) ? 0.0625f : 1.f;
             const __half hi = __float2half_rn(whole * by);
             const __half lo = __float2half_rn((z - whole) * by);
-            const int at = ((((p * 2) * kGr + g) * kHeads + hh) * 8 + i) * 8 + (n & 3) * 2 + (n >> 2);
+            const int at =
+                ((((p * 2) * kGr + g) * kHeads + hh) * 8 + i) * 8 + (n & 3) * 2 + (n >> 2);
             reinterpret_cast<__half*>(qf)[at] = hi;
             reinterpret_cast<__half*>(qf)[at + kGr * kHeads * 64] = lo;
           }
@@ -713,7 +717,9 @@ __global__ void __launch_bounds__(W * 32, W == kWarps ? kCtasPerSm : 1) decode_k
             for (int e = 0; e < kOwn; ++e)
               off[gr][e] = fmaf(pr[e], bf16_hi(par[sub][u]), off[gr][e]);
             if (kFew) few[kFew ? sub : 0][u][gr] = pr[0] * sc;
-            else wgt[kFew ? 0 : gr][sub][u] = transpose8x8(pack_half(pr[0] * sc, pr[kOwn - 1] * sc));
+            else
+              wgt[kFew ? 0 : gr][sub][u] =
+                  transpose8x8(pack_half(pr[0] * sc, pr[kOwn - 1] * sc));
           }
         if (!kFew) pv<D>(o, wgt[kFew ? 0 : gr], tile, gr, g, t4, down[gr]);
       }
@@ -786,7 +792,7 @@ __global__ void __launch_bounds__(W * 32, W == kWarps ? kCtasPerSm : 1) decode_k
       acc += f * mo[(w * kHeads + hh) * D + d];
       lsum += f * ml[w * kHeads + hh];
     }
-    if (whole_units) {
+    if (kWhole) {
       const size_t row = (size_t)seq * Hq + h_base + hh;
       O[row * D + d] = __float2bfloat16_rn(acc / lsum);
       if (d == 0) LSE[row] = (mu + log2f(lsum)) * 0.69314718055994530942f;
@@ -882,7 +888,7 @@ __global__ void __launch_bounds__(kMergeThreads) decode_merge(
 }
 
 namespace {
-std::atomic<unsigned long long> g_smem_set[8];  // by kernel: a bit a device
+std::atomic<unsigned long long> g_smem_set[12];  // by kernel: a bit a device
 }
 
 template <int D>
@@ -898,12 +904,15 @@ cudaError_t launch_decode_t(const void* q, const Pages& pg, const int* t, void* 
   const long long units = (long long)B * pg.Hkv * n_hg;
   const bool few = Hq / pg.Hkv <= 4, whole_units = takes_whole(units, cap);
   const bool wide = whole_units && units <= 148;
-  auto kern = wide ? (few ? decode_kernel<D, true, kWide> : decode_kernel<D, false, kWide>)
-                   : (few ? decode_kernel<D, true, kWarps> : decode_kernel<D, false, kWarps>);
+  auto kern =
+      wide ? (few ? decode_kernel<D, true, kWide, true> : decode_kernel<D, false, kWide, true>)
+      : whole_units
+          ? (few ? decode_kernel<D, true, kWarps, true> : decode_kernel<D, false, kWarps, true>)
+          : (few ? decode_kernel<D, true, kWarps, false> : decode_kernel<D, false, kWarps, false>);
   const int threads = (wide ? kWide : kWarps) * 32;
   const int smem = wide ? DecodeSmem<D, kWide>::kTotal : DecodeSmem<D, kWarps>::kTotal;
   // once a device: the attribute stays with the function there
-  std::atomic<unsigned long long>& set = g_smem_set[D / 128 * 4 + wide * 2 + few];
+  std::atomic<unsigned long long>& set = g_smem_set[D / 128 * 6 + (wide + whole_units) * 2 + few];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess && (dev >= 64 || !(set.load() >> dev & 1))) {
@@ -913,7 +922,7 @@ cudaError_t launch_decode_t(const void* q, const Pages& pg, const int* t, void* 
   if (e != cudaSuccess) return e;
   kern<<<whole_units ? (int)units : shares, threads, smem, stream>>>(
       static_cast<const __nv_bfloat16*>(q), pg, t, Opart, MLpart, static_cast<__nv_bfloat16*>(O),
-      LSE, B, Hq, s, c, scale * 1.4426950408889634f, n_hg, whole_units, make_theta(D, base));
+      LSE, B, Hq, s, c, scale * 1.4426950408889634f, n_hg, make_theta(D, base));
   e = cudaGetLastError();
   if (e != cudaSuccess || whole_units) return e;
   // Warps by the partials a unit has on average.  With few, a warp a head: 62

@@ -485,7 +485,8 @@ __global__ void __cluster_dims__(C, 1, 1) __launch_bounds__(kPlanThreads, 1) com
   if (tid == 0) w.head[16 + rank] = part_low;
   phase_end<C>();
   if (get<C>(w.head)) {
-    for (long long e = gid; e < (long long)B * max_blocks; e += kAll) table_out[e] = get<C>(w.table + e);
+    for (long long e = gid; e < (long long)B * max_blocks; e += kAll)
+      table_out[e] = get<C>(w.table + e);
     if (refs_out != refs_in)
       for (int p = gid; p < num_blocks; p += kAll) refs_out[p] = refs_in[p];
     for (int p = gid; p < num_blocks; p += kAll) moved[p] = p;
