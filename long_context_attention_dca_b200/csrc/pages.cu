@@ -82,32 +82,33 @@ struct Batch {
   }
 };
 
-// Exclusive prefix sum of one value a thread over the block; `total` gets the sum.
-__device__ __forceinline__ int block_scan(int v, int* warp_sums, int& total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int x = v;
-#pragma unroll
-  for (int sh = 1; sh < 32; sh <<= 1) {
-    const int y = __shfl_up_sync(0xFFFFFFFFu, x, sh);
-    if (lane >= sh) x += y;
+// Exclusive prefix sums of one value a thread over the block; `total` gets the sum.
+// One barrier each: every warp adds up the warps' sums for itself, and two sets of
+// them take turns.
+struct Scan {
+  int* sums;  // [2][32], shared
+  int turn;
+  __device__ explicit Scan(int* p) : sums(p), turn(0) {}
+  __device__ __forceinline__ int operator()(int v, int& total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int x = inclusive(v, lane);
+    if (lane == 31) sums[turn + warp] = x;
+    __syncthreads();
+    const int all = inclusive(sums[turn + lane], lane);
+    turn ^= 32;
+    total = __shfl_sync(0xFFFFFFFFu, all, 31);
+    const int before = __shfl_sync(0xFFFFFFFFu, all, warp ? warp - 1 : 0);
+    return (warp ? before : 0) + x - v;
   }
-  if (lane == 31) warp_sums[warp] = x;
-  __syncthreads();
-  if (warp == 0) {
-    int w = warp_sums[lane];
+  __device__ static __forceinline__ int inclusive(int x, int lane) {
 #pragma unroll
     for (int sh = 1; sh < 32; sh <<= 1) {
-      const int y = __shfl_up_sync(0xFFFFFFFFu, w, sh);
-      if (lane >= sh) w += y;
+      const int y = __shfl_up_sync(0xFFFFFFFFu, x, sh);
+      if (lane >= sh) x += y;
     }
-    warp_sums[lane] = w;
+    return x;
   }
-  __syncthreads();
-  const int before = (warp ? warp_sums[warp - 1] : 0) + x - v;
-  total = warp_sums[31];
-  __syncthreads();
-  return before;
-}
+};
 
 // Part of 0 .. n-1 that CTA `rank` scans: contiguous, so that a rank within the
 // part plus the parts before it is a rank in the whole.
@@ -209,8 +210,8 @@ __global__ void __cluster_dims__(C, 1, 1) __launch_bounds__(kPlanThreads, 1) rem
     const int* __restrict__ new_len, const int* table_in, int* table_out, const int* refs_in,
     int* refs_out, int* __restrict__ info, int B, int max_blocks, int num_blocks, int R,
     Work w) {
-  __shared__ int sums[32];
-  __shared__ int carry;
+  __shared__ int sums[64];
+  Scan block_scan(sums);
   const int rank = blockIdx.x, tid = threadIdx.x;
   const int gid = rank * kPlanThreads + tid;
   constexpr int kAll = C * kPlanThreads, kBatch = kBatchOf<C>;
@@ -305,13 +306,12 @@ __global__ void __cluster_dims__(C, 1, 1) __launch_bounds__(kPlanThreads, 1) rem
     for (int p = mine.begin + tid; p < mine.end; p += kPlanThreads)
       local += get<C>(w.count + p) == 0 && get<C>(w.owner + p) == kNone;
     int part_free;
-    block_scan(local, sums, part_free);
+    block_scan(local, part_free);
     if (tid == 0) w.head[8 + rank] = part_free;
   }
   // where each slot's new pages start among all new pages
   if (rank == 0) {
-    if (tid == 0) carry = 0;
-    __syncthreads();
+    int carry = 0;
     for (int b0 = 0; b0 < B; b0 += kPlanThreads) {
       const int b = b0 + tid;
       int need = 0, stay = 0;
@@ -324,14 +324,12 @@ __global__ void __cluster_dims__(C, 1, 1) __launch_bounds__(kPlanThreads, 1) rem
         need = get<C>(slot(w, kPages, B, b)) - stay;
       }
       int total;
-      const int before = block_scan(need, sums, total);
+      const int before = block_scan(need, total);
       if (b < B) {
         *slot(w, kUsed, B, b) = stay;
         *slot(w, kFresh, B, b) = carry + before - stay;
       }
-      __syncthreads();
-      if (tid == 0) carry += total;
-      __syncthreads();
+      carry += total;
     }
     if (tid == 0) w.head[2] = carry;
   }
@@ -357,7 +355,7 @@ __global__ void __cluster_dims__(C, 1, 1) __launch_bounds__(kPlanThreads, 1) rem
         free = n == 0;
       }
       int total;
-      const int at = before + block_scan(free, sums, total);
+      const int at = before + block_scan(free, total);
       if (p < mine.end) {
         if (free) {
           w.list[at] = p;
@@ -424,7 +422,8 @@ __global__ void __cluster_dims__(C, 1, 1) __launch_bounds__(kPlanThreads, 1) com
     const int* __restrict__ len, const int* table_in, int* table_out, const int* refs_in,
     int* refs_out, int* __restrict__ moved, int* __restrict__ info, int B, int max_blocks,
     int num_blocks, int R, Work w) {
-  __shared__ int sums[32];
+  __shared__ int sums[64];
+  Scan block_scan(sums);
   const int rank = blockIdx.x, tid = threadIdx.x;
   const int gid = rank * kPlanThreads + tid;
   constexpr int kAll = C * kPlanThreads, kBatch = kBatchOf<C>;
@@ -452,7 +451,7 @@ __global__ void __cluster_dims__(C, 1, 1) __launch_bounds__(kPlanThreads, 1) com
     bad |= n < 0;
   }
   int part_live;
-  block_scan(local, sums, part_live);
+  block_scan(local, part_live);
   if (tid == 0) w.head[8 + rank] = part_live;
   phase_end<C>();
   for (Entries at = first; at.b < B;) {
@@ -481,7 +480,7 @@ __global__ void __cluster_dims__(C, 1, 1) __launch_bounds__(kPlanThreads, 1) com
   for (int p = mine.begin + tid; p < min(mine.end, live); p += kPlanThreads)
     local += w.count[p] > 0;
   int part_low;
-  block_scan(local, sums, part_low);
+  block_scan(local, part_low);
   if (tid == 0) w.head[16 + rank] = part_low;
   phase_end<C>();
   if (get<C>(w.head)) {
@@ -503,7 +502,7 @@ __global__ void __cluster_dims__(C, 1, 1) __launch_bounds__(kPlanThreads, 1) com
     const int p = p0 + tid;
     const int used = p < mine.end && w.count[p] > 0;
     int total;
-    const int at = before + block_scan(used, sums, total);  // pages in use below p
+    const int at = before + block_scan(used, total);  // pages in use below p
     if (p < mine.end) {
       if (used && p >= live) w.from[at - low] = p;
       if (!used && p < live) w.to[p - at] = p;
