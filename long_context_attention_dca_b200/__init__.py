@@ -15,6 +15,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+import struct
 
 import torch
 
@@ -634,7 +635,7 @@ def dca_kv4_read_paged(pool, block_table, cu_seqlens, t0, T, D, K=None, V=None):
         raise DcaError(1, "K and V are given together or not at all")
     dev, out_rows = pool.device, 0
     if K is None:
-        K = torch.empty((T, Hkv, D), dtype=torch.bfloat16, device=dev)
+        K = pool.new_empty((T, Hkv, D), dtype=torch.bfloat16)
         V = torch.empty_like(K)
     else:
         packed = isinstance(K, torch.Tensor) and K.dim() == 3
@@ -695,14 +696,13 @@ def dca_attn_decode_kv4_paged(q, pool, block_table, t, s, c, base=10000.0, scale
     return O, LSE
 
 
-class _PagePool(ctypes.Structure):
-    _fields_ = [("base", _P), ("unit_bytes", _Z), ("outer", _I), ("unit_rows", _I)]
+_POOL = struct.Struct("PNii")  # dca_page_pool_t: base, unit_bytes, outer, unit_rows
 
 
 def _page_pools(pools, num_blocks, block_rows, dev):
-    """The descriptors of pools with pages of block_rows rows: bf16 [num_blocks,
-    block_rows, Hkv, D], 4-bit uint8 [num_blocks, Hkv, block_rows / 64, tile],
-    given one by one or stacked in one 5-d tensor."""
+    """The descriptors, packed, of pools with pages of block_rows rows: bf16
+    [num_blocks, block_rows, Hkv, D], 4-bit uint8 [num_blocks, Hkv, block_rows / 64,
+    tile], given one by one or stacked in one 5-d tensor; and their number."""
     found = []
     for p in [pools] if isinstance(pools, torch.Tensor) else pools:
         if not isinstance(p, torch.Tensor) or p.device != dev:
@@ -722,8 +722,8 @@ def _page_pools(pools, num_blocks, block_rows, dev):
                               f"{block_rows} rows")
         base = p.data_ptr()
         for i in range(shape[0] if lead else 1):
-            found.append((base + i * page * num_blocks, *desc))
-    return (_PagePool * max(1, len(found)))(*found), len(found)
+            found.append(_POOL.pack(base + i * page * num_blocks, *desc))
+    return b"".join(found), len(found)
 
 
 def _page_lists(B, *lists):
@@ -751,9 +751,10 @@ def dca_pages_workspace(B: int, max_blocks: int, num_blocks: int) -> int:
 def _page_scratch(refs, info, workspace, B, max_blocks):
     if info is None:
         info = refs.new_empty(2)
-    _need(info, "info", torch.int32, 1)
-    if info.numel() < 2:
-        raise DcaError(1, "info must have 2 entries")
+    else:
+        _need(info, "info", torch.int32, 1)
+        if info.numel() < 2:
+            raise DcaError(1, "info must have 2 entries")
     if workspace is None:
         workspace = refs.new_empty(-(-dca_pages_workspace(B, max_blocks, refs.numel()) // 4))
     return info, workspace
@@ -778,7 +779,7 @@ def dca_pages_remap(src, old_len, new_len, block_table, refs, pools, block_rows,
     _same_device(dev, src, old_len, new_len, block_table, table_out, counts_out, info, workspace)
     _call("dca_pages_remap", dev, src.data_ptr(), old_len.data_ptr(), new_len.data_ptr(),
           block_table.data_ptr(), refs.data_ptr(), table_out.data_ptr(), counts_out.data_ptr(),
-          info.data_ptr(), B, max_blocks, num_blocks, block_rows, ctypes.addressof(desc), n,
+          info.data_ptr(), B, max_blocks, num_blocks, block_rows, desc, n,
           workspace.data_ptr(), workspace.nbytes)
     return table_out, counts_out, info
 
@@ -801,7 +802,7 @@ def dca_pages_compact(lens, block_table, refs, pools, block_rows, workspace=None
     _same_device(dev, lens, block_table, table_out, counts_out, moved, info, workspace)
     _call("dca_pages_compact", dev, lens.data_ptr(), block_table.data_ptr(), refs.data_ptr(),
           table_out.data_ptr(), counts_out.data_ptr(), moved.data_ptr(), info.data_ptr(), B,
-          max_blocks, num_blocks, block_rows, ctypes.addressof(desc), n, workspace.data_ptr(),
+          max_blocks, num_blocks, block_rows, desc, n, workspace.data_ptr(),
           workspace.nbytes)
     return table_out, counts_out, moved, info
 

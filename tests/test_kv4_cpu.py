@@ -253,8 +253,13 @@ def test_decode_refusals(lib, want, args):
     assert _decode(lib, **args) == want
 
 
+class _PagePool(ctypes.Structure):
+    _fields_ = [("base", ctypes.c_void_p), ("unit_bytes", ctypes.c_size_t),
+                ("outer", ctypes.c_int), ("unit_rows", ctypes.c_int)]
+
+
 def _pool(base=0x30000, unit=256, outer=1, rows=1):
-    p = (dca._PagePool * 1)()
+    p = (_PagePool * 1)()
     p[0] = (base, unit, outer, rows)
     return ctypes.byref(p)
 
@@ -296,7 +301,7 @@ def test_page_refusals(lib, call, want, args):
 def test_page_pools_too_large_together(lib, call):
     # each page is 2^40 bytes, which one pool may have; 256 of them are more than
     # the copies can number
-    pools = (dca._PagePool * 256)(*[(0x30000, 1 << 20, 1 << 20, 64)] * 256)
+    pools = (_PagePool * 256)(*[(0x30000, 1 << 20, 1 << 20, 64)] * 256)
     assert call(lib, n=256, pools=ctypes.byref(pools)) == 2
 
 
