@@ -21,14 +21,14 @@
 // fp32: the codes are not centred, so a long sum inside the tensor core, which
 // truncates, would drift by more than the result can bear.
 //
-// Kernel 1, one CTA per (share of the cache, kv head, group of <= 8 query
-// heads, sequence): four warps take the share's 64-key tiles in turn, each
-// fetching its own tiles (K part and V part, 36 * D contiguous bytes each, one
-// bulk copy) through a small ring, so that the running maximum, its shuffles
-// and the update of O are paid once per 64 keys of a warp.  The sequence's
-// tiles are shared out evenly on the device from t[b], whatever the cache's
-// capacity.  Kernel 2 merges the shares.  Where the caches are short a CTA takes a
-// unit whole and there is no second kernel.
+// Kernel 1, a CTA per share of the tiles of all (sequence, kv head, group of <= 8
+// query heads): four warps take its 64-key tiles in turn, each fetching its own
+// (K part and V part, 36 * D contiguous bytes each, one bulk copy) through a small
+// ring, so that the running maximum, its shuffles and the update of O are paid
+// once per 64 keys of a warp.  The tiles are shared out evenly on the device from
+// t[b], whatever the caches' capacity.  Kernel 2 merges the shares.  Where the
+// caches are short a CTA takes a (sequence, kv head, group) whole and there is no
+// second kernel.
 //
 // What bounds it.  A key costs 144 bytes of cache a kv head (D = 128) and, with
 // eight query heads on it, about 18 instructions a warp (1145 for 64 keys, 96 of
@@ -78,11 +78,12 @@ constexpr int kSetup = 8;
 // 148 units of 100 / 500 / 1000 / 2000 keys, 8 query heads, 9.1 / 9.5 / 12.0 / 16.9
 // us against 12.8 / 16.9 / 19.6 / 22.8; 512 units 20.5 / 24.7 / 33.5 / 52.5 against
 // 22.3 / 28.3 / 37.8 / 54.5, and slower from 3000 keys on; 8 units 8.7 / 9.2 / 11.6 /
-// 16.4 against 10.5 / 10.9 / 10.2 / 10.4, where one launch fewer also saves 4 us
-// of the host's time, which is what such a call waits for outside a graph.
+// 16.4 against 10.5 / 10.9 / 10.2 / 10.4, where one launch fewer also saves 2 us
+// of the host's time, which is what such a call waits for outside a graph (962
+// keys, 8 heads: 15.7 us a call against 17.8).
 constexpr int kWide = 8;  // warps of such a CTA where every unit has an SM to itself: 1000 keys
                           // take 12.0 us, 13.8 with twelve, 14.6 with four
-constexpr long long kWholeUnits = 1 << 20;  // the launch grid
+constexpr long long kWholeUnits = 0x7FFFFFFF;  // the launch grid
 inline bool takes_whole(long long units, long long cap) {  // cap: rows of a cache
   return units <= kWholeUnits && cap <= (units < 64 ? 1024 : 2048);
 }
@@ -335,6 +336,7 @@ __global__ void __launch_bounds__(W * 32, W == kWarps ? kCtasPerSm : 1) decode_k
       }
       b_at += __shfl_sync(0xFFFFFFFFu, sum, 31);
       b += 32;
+      if (b >= B) return;  // t has changed meanwhile
       scan(b);
     }
   }
