@@ -702,18 +702,18 @@ __global__ void __launch_bounds__(W * 32, W == kWarps ? kCtasPerSm : 1) decode_k
             par[sub][u] = *reinterpret_cast<const uint32_t*>(vp + (sub * 16 + 2 * u) * (kGr * 4));
             most = max_bf16x2(most, par[sub][u]);
           }
-        // scale * 2^(14 - exponent of the tile's largest scale) < 2^15, by adding
-        // to the exponent (a scale of 0 becomes some number, which its codes of 0
-        // cancel; the offset of a NaN group is NaN as well)
+        // scale * 2^(14 - exponent of the tile's largest scale) < 2^15: a product, not
+        // a sum of exponents, which a scale of 0 or one far below the largest would
+        // leave; its factor is a normal number for every ex
         const uint32_t ex =
             max(__reduce_max_sync(0xFFFFFFFFu, most & 0xFFFFu) >> 7, 40u);
-        const uint32_t up = (141u - ex) << 23;
+        const float up = __uint_as_float((268u - ex) << 23);
         down[gr] = __uint_as_float((ex - 14u) << 23);
 #pragma unroll
         for (int sub = 0; sub < 4; ++sub)
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
-            const float sc = __uint_as_float(par[sub][u] * 65536u + up);
+            const float sc = bf16_lo(par[sub][u]) * up;
             const float* pr = x[sub] + u * kOwn;
 #pragma unroll
             for (int e = 0; e < kOwn; ++e)

@@ -1,0 +1,74 @@
+"""Decode over the 4-bit cache at the ends of the number ranges: values, keys
+and queries as large and as small as append and bf16 take them."""
+
+import numpy as np
+import pytest
+import torch
+
+import long_context_attention_dca_b200 as dca
+from oracle import kv4_oracle as ko
+from tests import kv4_util as ku
+from tests.test_gpu_kv4 import _close, _with_room
+
+pytestmark = pytest.mark.gpu
+
+# A table as long as its sequences (a block a unit) and a longer one (shares).
+ROWS = [0, 4096]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from long_context_attention_dca_b200 import build
+    build.build()
+    dca.lib()
+    yield
+    dca.dca_sync_status()
+
+
+def _decode(q, pool, table, t, s, c, rows, scale=0.0):
+    out = dca.dca_attn_decode_kv4_paged(q.cuda(), torch.from_numpy(pool).cuda(),
+                                        ku.ints(_with_room(table, rows, pool.shape[2] * 64)),
+                                        ku.ints(t), s, c, scale=scale)
+    dca.dca_sync_status()
+    return out
+
+
+def _forget_the_rest(pool, table, t, D):
+    """NaN parameters in every row past a sequence's last one."""
+    R = pool.shape[2] * 64
+    for b, x in enumerate(t):
+        for r in range(x % R + 1, R):
+            for h in range(pool.shape[1]):
+                for what in ("k", "v"):
+                    ko.write_row(pool[table[b, x // R], h, r // 64], what, r % 64,
+                                 np.full(D, 15, np.uint8), np.full(D // 64, np.nan),
+                                 np.full(D // 64, np.nan))
+
+
+@pytest.mark.parametrize("rows", ROWS)
+@pytest.mark.parametrize("G", [2, 8])
+@pytest.mark.parametrize("D", [64, 128])
+def test_decode_of_large_values_beside_constant_ones(D, G, rows):
+    # Every tile, a partly filled last one too, has a row of the stated scale, rows of
+    # equal values (their scale is 0, as append stores them) and ordinary rows.
+    rng, gen = np.random.default_rng(41), torch.Generator().manual_seed(41)
+    Hkv, R, s, c = 2, 64, 40, 60
+    t = [100, 68, 30]
+    q = ku.bf16_rows(gen, len(t), Hkv * G, D)
+    for power in (13, 14, 15, 16, 17, 20, 100, 118):
+        table, num = ku.random_tables(rng, [x + 1 for x in t], R)
+        pool = ku.random_pool(rng, num, Hkv, R, D)
+        _forget_the_rest(pool, table, t, D)
+        gr = D // 64
+        for b, x in enumerate(t):
+            for first in range(0, x + 1, 64):
+                for h in range(Hkv):
+                    tile = ko._tile(pool, table, b, first, h)
+                    big = np.full(gr, 1.5 * 2.0 ** power)
+                    ko.write_row(tile, "v", 1, rng.integers(0, 16, D).astype(np.uint8), big,
+                                 -7 * big)
+                    zero = np.zeros(D, np.uint8)
+                    ko.write_row(tile, "v", 0, zero, np.zeros(gr), np.zeros(gr))
+                    ko.write_row(tile, "v", 3, zero, np.zeros(gr), big)
+        got = _decode(q, pool, table, t, s, c, rows)
+        _close(got, ko.decode(ku.f64(q), pool, table, t, s, c), (power, rows))
