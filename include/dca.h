@@ -530,7 +530,8 @@ size_t dca_attn_decode_kv4_workspace(int B, int Hq, int Hkv, int D, int Tcap);
  * base, scale as dca_attn_decode.  Rows past t[b] may hold anything.  The
  * rotated query enters the scores with 22 bits of its head's largest value and
  * the codes exactly; P times the value scale is rounded to fp16 (11 bits, relative
- * to the largest scale among 64 neighbouring keys).  A t[b] outside the cache,
+ * to the largest scale among 64 neighbouring keys, or to 2^-113 where that is
+ * larger).  A t[b] outside the cache,
  * or a table entry outside [0, num_blocks) that the sequence reads, is reported
  * by dca_sync_status (INVALID_ARG) and that sequence's outputs are NaN.  Two
  * calls that overlap on the GPU need a workspace each.

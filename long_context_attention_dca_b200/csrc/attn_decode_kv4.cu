@@ -16,8 +16,8 @@
 //     O = sum_j (p_j scale_j) c_j + sum_j p_j offset_j,
 // again on the bare codes, with p_j scale_j rounded to fp16 after a
 // normalisation by the largest scale of the 64-key tile (a power of two), so
-// that any range of scales fits; the second sum stays in fp32 outside the
-// matrix product.  A tile's product is formed from zero and then added to O in
+// that scales of any size from 2^-113 on fit; the second sum stays in fp32 outside
+// the matrix product.  A tile's product is formed from zero and then added to O in
 // fp32: the codes are not centred, so a long sum inside the tensor core, which
 // truncates, would drift by more than the result can bear.
 //
@@ -483,8 +483,9 @@ __global__ void __launch_bounds__(W * 32, W == kWarps ? kCtasPerSm : 1) decode_k
   const int head0 = kFew ? t4 : 2 * t4;
   float m_run[kOwn], l_run[kOwn];
   float off[kGr][kOwn];       // sum of p * offset, by group
-  // O of 16 dims: rows g and g + 8, each kOwn heads; times 2^-24, rows g + 8 times
-  // 16 besides
+  // O of 16 dims: rows g and g + 8, each kOwn heads; times 2^-10, rows g + 8 times
+  // 16 besides.  (Products come times 2^14 for the weights and 2^-24 for the codes;
+  // the two together, left alone, keep the least and the largest scales in range.)
   float o[kGr * 4][2 * kOwn];
 #pragma unroll
   for (int e = 0; e < kOwn; ++e) {
@@ -704,11 +705,12 @@ __global__ void __launch_bounds__(W * 32, W == kWarps ? kCtasPerSm : 1) decode_k
           }
         // scale * 2^(14 - exponent of the tile's largest scale) < 2^15: a product, not
         // a sum of exponents, which a scale of 0 or one far below the largest would
-        // leave; its factor is a normal number for every ex
+        // leave; its factor is a normal number for every ex (from a largest scale of
+        // 2^-113 on; smaller ones count as that)
         const uint32_t ex =
-            max(__reduce_max_sync(0xFFFFFFFFu, most & 0xFFFFu) >> 7, 40u);
+            max(__reduce_max_sync(0xFFFFFFFFu, most & 0xFFFFu) >> 7, 14u);
         const float up = __uint_as_float((268u - ex) << 23);
-        down[gr] = __uint_as_float((ex - 14u) << 23);
+        down[gr] = __uint_as_float(ex << 23);
 #pragma unroll
         for (int sub = 0; sub < 4; ++sub)
 #pragma unroll
@@ -768,8 +770,8 @@ __global__ void __launch_bounds__(W * 32, W == kWarps ? kCtasPerSm : 1) decode_k
         for (int e = 0; e < kOwn; ++e) {
           // rows g and g + 8 are dims 2m and 2m + 1 of word g
           float* at = mo + (warp * kHeads + head0 + e) * D + gr * 64 + 8 * g + 2 * m;
-          at[0] = fmaf(o[gr * 4 + m][e], 16777216.f, off[gr][e]);        // 2^24
-          at[1] = fmaf(o[gr * 4 + m][kOwn + e], 1048576.f, off[gr][e]);  // 2^24 / 16
+          at[0] = fmaf(o[gr * 4 + m][e], 1024.f, off[gr][e]);        // 2^10
+          at[1] = fmaf(o[gr * 4 + m][kOwn + e], 64.f, off[gr][e]);   // 2^10 / 16
         }
     if (g == 0) {
 #pragma unroll

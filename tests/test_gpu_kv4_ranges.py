@@ -72,3 +72,37 @@ def test_decode_of_large_values_beside_constant_ones(D, G, rows):
                     ko.write_row(tile, "v", 3, zero, np.zeros(gr), big)
         got = _decode(q, pool, table, t, s, c, rows)
         _close(got, ko.decode(ku.f64(q), pool, table, t, s, c), (power, rows))
+
+
+def _params(pool, D, what):
+    """The bf16 parameters of all keys or values, uint16, as a view."""
+    gr, nb = D // 64, 32 * D
+    first = nb if what == "k" else 2 * nb + 256 * gr
+    return pool[..., first:first + 256 * gr].view(np.uint16)
+
+
+def _scaled(pool, D, what, power):
+    """The pool with all scales and offsets of the keys or values times 2^power."""
+    out = pool.copy()
+    words = _params(out, D, what)
+    words += np.array(power << 7).astype(np.uint16)  # to the exponent, modulo 2^16
+    return out
+
+
+@pytest.mark.parametrize("rows", ROWS)
+@pytest.mark.parametrize("G", [2, 8])
+@pytest.mark.parametrize("D", [64, 128])
+def test_decode_scales_with_its_values(D, G, rows):
+    # Every step up to the output's rounding commutes with a power of two as long as
+    # nothing leaves the normal range, so the outputs are the same bits, moved.
+    rng, gen = np.random.default_rng(42), torch.Generator().manual_seed(42)
+    Hkv, R, s, c, t = 2, 64, 40, 60, [100, 68, 30]
+    q = ku.bf16_rows(gen, len(t), Hkv * G, D)
+    table, num = ku.random_tables(rng, [x + 1 for x in t], R)
+    pool = ku.random_pool(rng, num, Hkv, R, D)
+    O, LSE = _decode(q, pool, table, t, s, c, rows)
+    _close((O, LSE), ko.decode(ku.f64(q), pool, table, t, s, c))
+    for power in (-100, -85, -40, 14, 17, 40, 115):
+        Ok, Lk = _decode(q, _scaled(pool, D, "v", power), table, t, s, c, rows)
+        assert torch.equal(Lk, LSE), power
+        assert torch.equal(Ok.double(), O.double() * 2.0 ** power), power
