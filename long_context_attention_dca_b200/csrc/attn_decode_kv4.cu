@@ -428,16 +428,28 @@ __global__ void __launch_bounds__(W * 32, W == kWarps ? kCtasPerSm : 1) decode_k
     for (int job = warp; job < (p_hi - p_lo + 1) * n_heads; job += W) {
       const int p = p_lo + job / n_heads, hh = job % n_heads;  // a piece and a head
       float x0[kPairs], x1[kPairs], big = 0.f;
+      // by the head's largest element first, so that queries of any size have the
+      // same bits behind them
 #pragma unroll
       for (int u = 0; u < kPairs; ++u) {
-        x0[u] = __bfloat162float(qraw[hh * D + lane + 32 * u]) * scale_log2;
-        x1[u] = __bfloat162float(qraw[hh * D + lane + 32 * u + D / 2]) * scale_log2;
+        x0[u] = __bfloat162float(qraw[hh * D + lane + 32 * u]);
+        x1[u] = __bfloat162float(qraw[hh * D + lane + 32 * u + D / 2]);
+        big = fmaxf(big, fmaxf(fabsf(x0[u]), fabsf(x1[u])));
+      }
+      const int most = (int)(__reduce_max_sync(~0u, __float_as_uint(big)) >> 23) - 127;
+      const int er = max(-126, min(most, 126));
+      const float whole_q = power2(-er);
+      big = 0.f;
+#pragma unroll
+      for (int u = 0; u < kPairs; ++u) {
+        x0[u] = x0[u] * whole_q * scale_log2;
+        x1[u] = x1[u] * whole_q * scale_log2;
         big = fmaxf(big, fabsf(x0[u]) + fabsf(x1[u]));
       }
-#pragma unroll
-      for (int sh = 16; sh >= 1; sh >>= 1) big = fmaxf(big, __shfl_xor_sync(~0u, big, sh));
-      // every rotated value times 2^-e stays below 2^11
-      const int e = big > 0.f ? (int)(__float_as_uint(big) >> 23) - 127 - 10 : 0;
+      big = __uint_as_float(__reduce_max_sync(~0u, __float_as_uint(big)));
+      // every rotated value times 2^-e stays below 2^11; scores come times 2^-(e + er + 24),
+      // which is to be a normal number (smaller ones are nothing to any key)
+      const int e = max(big > 0.f ? (int)(__float_as_uint(big) >> 23) - 127 - 10 : 0, -150 - er);
       const float down = power2(-(e / 2)), down2 = power2(-(e - e / 2));
       {
         float sum[2] = {0.f, 0.f};
@@ -449,11 +461,11 @@ __global__ void __launch_bounds__(W * 32, W == kWarps ? kCtasPerSm : 1) decode_k
 #pragma unroll
           for (int v = 0; v < 2; ++v) {
             const int d = k + v * (D / 2);
-            sum[D == 128 ? v : 0] += y[v];
             // nibbles 0..3 of a word go to the low halves of four registers,
             // 4..7 to the high halves; odd nibbles arrive times 16
             const int g = d / 64, i = (d % 64) / 8, n = d % 8;
             const float z = y[v] * down * down2, whole = rintf(z), by = (n & 1) ? 0.0625f : 1.f;
+            sum[D == 128 ? v : 0] += z;
             const __half hi = __float2half_rn(whole * by);
             const __half lo = __float2half_rn((z - whole) * by);
             const int at =
@@ -467,10 +479,10 @@ __global__ void __launch_bounds__(W * 32, W == kWarps ? kCtasPerSm : 1) decode_k
 #pragma unroll
           for (int g = 0; g < kGr; ++g) sum[g] += __shfl_xor_sync(~0u, sum[g], sh);
         // in the units of the code products
-        const float unit = down * down2 * 5.9604644775390625e-8f;  // 2^-24
+        const float unit = 5.9604644775390625e-8f;  // 2^-24
         if (lane < kGr) qsum[(p * kHeads + hh) * kGr + lane] = (lane == 0 ? sum[0] : sum[1]) * unit;
       }
-      if (lane == 0 && p == p_lo) qexp[hh] = power2(e + 24);
+      if (lane == 0 && p == p_lo) qexp[hh] = power2(e + er + 24);
     }
     __syncthreads();
   }

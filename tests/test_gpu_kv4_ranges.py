@@ -106,3 +106,41 @@ def test_decode_scales_with_its_values(D, G, rows):
         Ok, Lk = _decode(q, _scaled(pool, D, "v", power), table, t, s, c, rows)
         assert torch.equal(Lk, LSE), power
         assert torch.equal(Ok.double(), O.double() * 2.0 ** power), power
+
+
+def _signed_rows(gen, *shape):
+    """bf16 values of size 1 to 2, which any power of two keeps exact."""
+    x = 1 + torch.randint(0, 128, shape, generator=gen) / 128.0
+    return torch.where(torch.rand(shape, generator=gen) < 0.5, -x, x).to(torch.bfloat16)
+
+
+@pytest.mark.parametrize("rows", ROWS)
+@pytest.mark.parametrize("G", [2, 8])
+@pytest.mark.parametrize("D", [64, 128])
+def test_decode_of_small_queries_over_large_keys(D, G, rows):
+    # scores of a query times 2^-p over keys times 2^p are the same bits
+    rng, gen = np.random.default_rng(43), torch.Generator().manual_seed(43)
+    Hkv, R, s, c, t = 2, 64, 40, 60, [100, 68, 30]
+    q = _signed_rows(gen, len(t), Hkv * G, D)
+    table, num = ku.random_tables(rng, [x + 1 for x in t], R)
+    pool = ku.random_pool(rng, num, Hkv, R, D)
+    O, LSE = _decode(q, pool, table, t, s, c, rows)
+    _close((O, LSE), ko.decode(ku.f64(q), pool, table, t, s, c))
+    for power in (60, 100, 110, 114, 118, 122):
+        got = _decode(q * 2.0 ** -power, _scaled(pool, D, "k", power), table, t, s, c, rows)
+        assert torch.equal(got[1], LSE) and torch.equal(got[0], O), power
+
+
+@pytest.mark.parametrize("rows", ROWS)
+@pytest.mark.parametrize("D,G", [(64, 2), (128, 8), (128, 1), (64, 12)])
+def test_decode_of_queries_and_scales_next_to_nothing(D, G, rows):
+    rng, gen = np.random.default_rng(44), torch.Generator().manual_seed(44)
+    Hkv, R, s, c, t = 2, 64, 40, 60, [100, 68, 0]
+    table, num = ku.random_tables(rng, [x + 1 for x in t], R)
+    pool = ku.random_pool(rng, num, Hkv, R, D)
+    for size, scale in ((4e-35, 0.0), (1e-35, 0.0), (1e-38, 0.0), (1e-40, 0.0), (1.0, 1e-36),
+                        (1e-30, 1e-20), (1.0, -1e-37), (1e-36, 1e37)):
+        q = (torch.randn(len(t), Hkv * G, D, generator=gen) * size).to(torch.bfloat16)
+        q[0, 0] = 0.0
+        got = _decode(q, pool, table, t, s, c, rows, scale)
+        _close(got, ko.decode(ku.f64(q), pool, table, t, s, c, scale=scale), (size, scale))
