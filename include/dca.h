@@ -531,7 +531,9 @@ size_t dca_attn_decode_kv4_workspace(int B, int Hq, int Hkv, int D, int Tcap);
  * rotated query enters the scores with 22 bits of its head's largest value and
  * the codes exactly; P times the value scale is rounded to fp16 (11 bits, relative
  * to the largest scale among 64 neighbouring keys, or to 2^-113 where that is
- * larger).  A t[b] outside the cache,
+ * larger).  Queries, keys and values may have any finite size; a score, or a sum of
+ * exp(score - largest score) times values, past fp32's range (3.4e38) makes its
+ * head's outputs infinite or NaN.  A t[b] outside the cache,
  * or a table entry outside [0, num_blocks) that the sequence reads, is reported
  * by dca_sync_status (INVALID_ARG) and that sequence's outputs are NaN.  Two
  * calls that overlap on the GPU need a workspace each.

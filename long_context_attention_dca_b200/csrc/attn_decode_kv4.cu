@@ -132,7 +132,7 @@ struct DecodeSmem {
   static constexpr int kCs = 3 * (D / 2) * 8;          // cos, sin
   static constexpr int kRaw = kHeads * D * 2;          // queries as they came
   static constexpr int kSums = 3 * kHeads * (D / 64) * 4;  // sum of q per group
-  static constexpr int kF = kHeads * 4;
+  static constexpr int kF = 2 * kHeads * 4;  // power of two of a head's scores, in two parts
   static constexpr int kBars = W * kRing * 8 + 16;  // + abort and page words
   static constexpr int kPlaces = kMaxTiles * 4;  // pool tile of every tile of the share
   static constexpr int kTotal = kRings + kQ + kRaw + kCs + kSums + kF + kBars + kPlaces;
@@ -183,6 +183,7 @@ __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
   return *reinterpret_cast<const uint32_t*>(&m);
 }
 
+constexpr float kMostF = 1.7014118346046923e38f;  // 2^127
 // 2^e for e > -127; infinite above 127.
 __device__ __forceinline__ float power2(int e) {
   return __uint_as_float((unsigned)min(e + 127, 255) << 23);
@@ -267,8 +268,8 @@ __global__ void __launch_bounds__(W * 32, W == kWarps ? kCtasPerSm : 1) decode_k
   __nv_bfloat16* qraw = reinterpret_cast<__nv_bfloat16*>(qf + SM::kQ);
   float2* cs = reinterpret_cast<float2*>(qf + SM::kQ + SM::kRaw);
   float* qsum = reinterpret_cast<float*>(qf + SM::kQ + SM::kRaw + SM::kCs);  // [piece][head][group]
-  float* qexp = qsum + 3 * kHeads * kGr;                          // [head]
-  uint8_t* bars = reinterpret_cast<uint8_t*>(qexp + kHeads);
+  float* qexp = qsum + 3 * kHeads * kGr;                          // [2][head]
+  uint8_t* bars = reinterpret_cast<uint8_t*>(qexp + 2 * kHeads);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + W * kRing * 8);
   volatile int* bad_pages = abort_flag + 1;  // [2], of this piece and of the next
   uint32_t* places = reinterpret_cast<uint32_t*>(bars + SM::kBars);
@@ -286,7 +287,7 @@ __global__ void __launch_bounds__(W * 32, W == kWarps ? kCtasPerSm : 1) decode_k
   }
   for (int i = tid; i < SM::kQ / 16; i += kThreads)  // heads a unit does not have
     reinterpret_cast<uint4*>(qf)[i] = make_uint4(0, 0, 0, 0);
-  for (int i = tid; i < 3 * kHeads * kGr + kHeads; i += kThreads) qsum[i] = 0.f;
+  for (int i = tid; i < 3 * kHeads * kGr + 2 * kHeads; i += kThreads) qsum[i] = 0.f;
   // spans of 32 sequences, and those of the ones up to the lane's
   long long mine, sum;
   auto scan = [&](int first) {
@@ -482,7 +483,10 @@ __global__ void __launch_bounds__(W * 32, W == kWarps ? kCtasPerSm : 1) decode_k
         const float unit = 5.9604644775390625e-8f;  // 2^-24
         if (lane < kGr) qsum[(p * kHeads + hh) * kGr + lane] = (lane == 0 ? sum[0] : sum[1]) * unit;
       }
-      if (lane == 0 && p == p_lo) qexp[hh] = power2(e + er + 24);
+      if (lane == 0 && p == p_lo) {
+        qexp[hh] = power2(min(e + er + 24, 127));
+        qexp[kHeads + hh] = power2(max(0, min(e + er + 24 - 127, 127)));
+      }
     }
     __syncthreads();
   }
@@ -649,6 +653,13 @@ __global__ void __launch_bounds__(W * 32, W == kWarps ? kCtasPerSm : 1) decode_k
               if (j0 + sub * 16 + kr + 2 * u > j1) x[sub][u * kOwn + e] = -INFINITY;
       }
       next_part();
+      // a query too large for one power of two (above about 2^115)
+      if (fmaxf(F[0], F[kOwn - 1]) == kMostF) {
+#pragma unroll
+        for (int sub = 0; sub < 4; ++sub)
+#pragma unroll
+          for (int e = 0; e < 2 * kOwn; ++e) x[sub][e] *= qexp[kHeads + head0 + e % kOwn];
+      }
       float mx[kOwn];
       bool higher = false;
 #pragma unroll

@@ -144,3 +144,40 @@ def test_decode_of_queries_and_scales_next_to_nothing(D, G, rows):
         q[0, 0] = 0.0
         got = _decode(q, pool, table, t, s, c, rows, scale)
         _close(got, ko.decode(ku.f64(q), pool, table, t, s, c, scale=scale), (size, scale))
+
+
+@pytest.mark.parametrize("rows", ROWS)
+@pytest.mark.parametrize("G", [2, 8])
+@pytest.mark.parametrize("D", [64, 128])
+def test_decode_of_large_queries_over_small_keys(D, G, rows):
+    # The same scores as of the unscaled query and keys, but a score's sums leave
+    # fp32's normal range: five roundings of 2^-150 each.  In the units of the largest
+    # query element, below 4 * 2^power / sqrt(D) * log2(e) = 2^(power + .03 or .53), which
+    # is kept below 2^11 with codes in units of 2^-24, that is 5 * 2^-150 *
+    # 2^(power + 1 - 11 + 24) of a score, twice that of a weight.
+    rng, gen = np.random.default_rng(45), torch.Generator().manual_seed(45)
+    Hkv, R, s, c, t = 2, 64, 40, 60, [100, 68, 30]
+    q = _signed_rows(gen, len(t), Hkv * G, D)
+    table, num = ku.random_tables(rng, [x + 1 for x in t], R)
+    pool = ku.random_pool(rng, num, Hkv, R, D)
+    O, LSE, bO, bL = ko.decode(ku.f64(q), pool, table, t, s, c)
+    for power in (100, 112, 115, 118):
+        got = _decode(q * 2.0 ** power, _scaled(pool, D, "k", -power), table, t, s, c, rows)
+        more = 5 * 2.0 ** (power + 14 - 150)
+        # a value is at most 15 * 0.6 + 7.5 * 0.6 here
+        _close(got, (O, LSE, bO + 2 * more * 13.5, bL + more), power)
+
+
+@pytest.mark.parametrize("rows", ROWS)
+@pytest.mark.parametrize("D,G", [(64, 2), (128, 8)])
+def test_decode_of_the_largest_queries_over_keys_of_zero(D, G, rows):
+    # every score is 0: LSE is ln of the number of keys, the output their mean value
+    rng, gen = np.random.default_rng(46), torch.Generator().manual_seed(46)
+    Hkv, R, s, c, t = 2, 64, 40, 60, [100, 68, 30]
+    q = (torch.randn(len(t), Hkv * G, D, generator=gen) * 1e38).clamp(-3.3e38, 3.3e38)
+    q = q.to(torch.bfloat16)
+    table, num = ku.random_tables(rng, [x + 1 for x in t], R)
+    pool = ku.random_pool(rng, num, Hkv, R, D)
+    pool[..., :32 * D + 256 * (D // 64)] = 0  # codes and parameters of the keys
+    got = _decode(q, pool, table, t, s, c, rows)
+    _close(got, ko.decode(ku.f64(q), pool, table, t, s, c))
