@@ -85,8 +85,9 @@ struct Batch {
 // Exclusive prefix sums of one value a thread over the block; `total` gets the sum.
 // One barrier each: every warp adds up the warps' sums for itself, and two sets of
 // them take turns.
+constexpr int kScanInts = 2 * 32;
 struct Scan {
-  int* sums;  // [2][32], shared
+  int* sums;  // [kScanInts], shared
   int turn;
   __device__ explicit Scan(int* p) : sums(p), turn(0) {}
   __device__ __forceinline__ int operator()(int v, int& total) {
@@ -210,7 +211,7 @@ __global__ void __cluster_dims__(C, 1, 1) __launch_bounds__(kPlanThreads, 1) rem
     const int* __restrict__ new_len, const int* table_in, int* table_out, const int* refs_in,
     int* refs_out, int* __restrict__ info, int B, int max_blocks, int num_blocks, int R,
     Work w) {
-  __shared__ int sums[64];
+  __shared__ int sums[kScanInts];
   Scan block_scan(sums);
   const int rank = blockIdx.x, tid = threadIdx.x;
   const int gid = rank * kPlanThreads + tid;
@@ -422,7 +423,7 @@ __global__ void __cluster_dims__(C, 1, 1) __launch_bounds__(kPlanThreads, 1) com
     const int* __restrict__ len, const int* table_in, int* table_out, const int* refs_in,
     int* refs_out, int* __restrict__ moved, int* __restrict__ info, int B, int max_blocks,
     int num_blocks, int R, Work w) {
-  __shared__ int sums[64];
+  __shared__ int sums[kScanInts];
   Scan block_scan(sums);
   const int rank = blockIdx.x, tid = threadIdx.x;
   const int gid = rank * kPlanThreads + tid;
@@ -623,7 +624,8 @@ cudaError_t alone_bytes(K kern, int B, int max_blocks, int num_blocks, size_t& b
   bytes = 0;
   if (ints > kAloneInts) return cudaSuccess;
   bytes = ints * sizeof(int);
-  return bytes <= 48 << 10
+  // 48 KB without asking, the kernel's own arrays included
+  return bytes + kScanInts * sizeof(int) <= 48 << 10
              ? cudaSuccess
              : cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     (int)(kAloneInts * sizeof(int)));
