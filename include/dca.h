@@ -548,7 +548,10 @@ dca_status_t dca_attn_decode_kv4_paged(const void* q, const void* pool, const in
  * outer * (block_rows / unit_rows) * unit_bytes bytes at base + p * page_bytes,
  * [outer][block_rows / unit_rows][unit_bytes]; a partial page is copied in
  * units of unit_rows rows.  A bf16 pool [num_blocks][block_rows][Hkv][D] is
- * {base, 2 * Hkv * D, 1, 1}; a 4-bit pool {base, 72 * D, Hkv, 64}. */
+ * {base, 2 * Hkv * D, 1, 1}; a 4-bit pool {base, 72 * D, Hkv, 64}.  A call takes
+ * 0 to DCA_MAX_PAGE_POOLS of them (a model's keys and values of all layers: the
+ * pages of every pool move with the one block table); more are INVALID_ARG. */
+#define DCA_MAX_PAGE_POOLS 256
 typedef struct dca_page_pool {
   void* base;        /* device, 16-byte aligned                 */
   size_t unit_bytes; /* a multiple of 16                        */

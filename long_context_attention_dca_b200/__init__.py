@@ -764,8 +764,8 @@ def dca_pages_remap(src, old_len, new_len, block_table, refs, pools, block_rows,
                     block_table_out=None, refs_out=None, info=None):
     """One step of the slots over paged pools (fork, share, reorder, cut, grow,
     free; see dca.h).  src, old_len, new_len int32 [B]; block_table int32 [B,
-    max_blocks]; refs int32 [num_blocks]; pools: tensors whose partial pages are
-    copied, one by one or stacked.  Returns (block_table, refs, info), new
+    max_blocks]; refs int32 [num_blocks]; pools: up to 256 tensors whose partial
+    pages are copied, one by one or stacked (a layer each).  Returns (block_table, refs, info), new
     tensors unless given (a given one may be the one it replaces)."""
     _need(block_table, "block_table", torch.int32, 2)
     _need(refs, "refs", torch.int32, 1)

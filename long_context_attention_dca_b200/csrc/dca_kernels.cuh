@@ -166,7 +166,7 @@ struct PoolDesc {
   int outer, unit_rows;
   int chunks, items;  // per part and per page (filled by the launcher)
 };
-constexpr int kMaxPools = 256;
+constexpr int kMaxPools = DCA_MAX_PAGE_POOLS;
 template <int N>
 struct Pools {
   long long items;  // of one page over all pools (filled by the launcher)

@@ -11,6 +11,7 @@ import torch
 import long_context_attention_dca_b200 as dca
 from oracle import kv4_oracle as ko
 from tests import kv4_util as ku
+from tests.test_gpu_pages import _moved, _remap
 
 pytestmark = pytest.mark.gpu
 
@@ -60,3 +61,53 @@ def test_plans_that_just_pass_the_default_shared_memory():
     res = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True,
                          timeout=600)
     assert res.returncode == 0, res.stderr[-2000:]
+
+
+def _pools(num, R, n, seed):
+    """n pools of three kinds, whose pages are 8 KB, 128 KB and 2 x 4.5 KB."""
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    out = []
+    for j in range(n):
+        if j % 3 == 2:
+            out.append(torch.randint(0, 256, (num, 2, R // 64, 4608), generator=gen, device="cuda",
+                                     dtype=torch.uint8))
+        else:
+            shape = (num, R, 1, 64) if j % 3 == 0 else (num, R, 8, 128)
+            out.append(torch.randn(shape, generator=gen, device="cuda").to(torch.bfloat16))
+    return out
+
+
+@pytest.mark.parametrize("n", [1, 15, 16, 17, 64, 255, 256])
+def test_pools_of_many_layers(n):
+    rng = np.random.default_rng(n)
+    R, B = 64, 5
+    lens, table, refs, num = ku.random_slots(rng, B, 4, R, extra=12)
+    src = [0, 0, 2, 2, -1]
+    new = [min(4 * R, lens[f] + 1) if f >= 0 else 70 for f in src]
+    pools = _pools(num, R, n, n)
+    want = ko.remap(src, lens, new, table, refs, R)
+    assert want[2][1] > 0
+    expect = _moved(pools, want[3])
+    got = _remap(src, lens, new, table, refs, pools, R)
+    dca.dca_sync_status()
+    assert got == tuple(want[:3])
+    assert all(torch.equal(a, b) for a, b in zip(pools, expect))
+    table, refs = want[:2]
+    want = ko.compact(new, table, refs, R)
+    assert want[3][1] > 0
+    expect = _moved(pools, want[4])
+    got = dca.dca_pages_compact(ku.ints(new), ku.ints(table), ku.ints(refs), pools, R)
+    dca.dca_sync_status()
+    assert tuple(x.tolist() for x in got) == tuple(want[:4])
+    assert all(torch.equal(a, b) for a, b in zip(pools, expect))
+
+
+def test_more_pools_than_a_call_takes_are_refused():
+    stacked = torch.zeros(257, 3, 64, 1, 64, dtype=torch.bfloat16, device="cuda")
+    state = ([0], [10], [11], [[2]], [0, 0, 1])
+    with pytest.raises(dca.DcaError, match="256"):
+        _remap(*state, stacked, 64)
+    with pytest.raises(dca.DcaError, match="256"):
+        dca.dca_pages_compact(ku.ints([10]), ku.ints([[2]]), ku.ints([0, 0, 1]), stacked, 64)
+    assert _remap(*state, stacked[1:], 64) == ([[2]], [0, 0, 1], [2, 0])
+    dca.dca_sync_status()
