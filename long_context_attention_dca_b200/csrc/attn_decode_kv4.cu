@@ -964,6 +964,14 @@ cudaError_t launch_decode_t(const void* q, const Pages& pg, const int* t, void* 
 
 }  // namespace kv4
 
+// Units, shares and a sequence's query elements (with a block's step) are counted in
+// ints.
+bool kv4_decode_fits(int B, int Hq, int Hkv, int D, long long cap) {
+  constexpr long long kMost = 0x7FFFFFFF;
+  return (long long)Hq * D <= 1 << 30 && (long long)B * Hkv * kv4::head_groups(Hq, Hkv) <= kMost &&
+         kv4::decode_shares(B, Hq, Hkv, cap) <= kMost;
+}
+
 size_t kv4_decode_workspace_bytes(int B, int Hq, int Hkv, int D, long long cap) {
   const size_t units = (size_t)B * Hkv * kv4::head_groups(Hq, Hkv);
   const size_t slots = units + (size_t)kv4::decode_shares(B, Hq, Hkv, cap);

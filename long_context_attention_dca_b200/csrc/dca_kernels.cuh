@@ -152,7 +152,8 @@ cudaError_t launch_kv4_read(const void* pool, const int* block_table, int max_bl
                             int block_rows, int num_blocks, const int* cu, const int* t0,
                             void* K, void* V, int B, int T, int Hkv, int D, int out_rows,
                             cudaStream_t stream);
-// Decode over it (cap = max_blocks * block_rows).
+// Decode over it (cap = max_blocks * block_rows), for shapes within the launch grid.
+bool kv4_decode_fits(int B, int Hq, int Hkv, int D, long long cap);
 size_t kv4_decode_workspace_bytes(int B, int Hq, int Hkv, int D, long long cap);
 cudaError_t launch_kv4_decode(const void* q, const void* pool, const int* block_table,
                               int max_blocks, int block_rows, int num_blocks, const int* t,

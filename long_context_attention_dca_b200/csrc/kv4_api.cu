@@ -78,6 +78,7 @@ dca_status_t dca_kv4_read_paged(const void* pool, const int* block_table, int ma
 
 size_t dca_attn_decode_kv4_workspace(int B, int Hq, int Hkv, int D, int Tcap) {
   if (B < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv || (D != 64 && D != 128) || Tcap < 1) return 0;
+  if (!kv4_decode_fits(B, Hq, Hkv, D, Tcap)) return 0;
   return kv4_decode_workspace_bytes(B, Hq, Hkv, D, Tcap);
 }
 
@@ -93,15 +94,17 @@ dca_status_t dca_attn_decode_kv4_paged(const void* q, const void* pool, const in
     st = check_kv4(fn, B, 1, Hkv, D, block_table, max_blocks, block_rows, num_blocks);
   if (st != DCA_OK) return st;
   if (B == 0) return DCA_OK;
-  if ((long long)Hkv * ((Hq / Hkv + 7) / 8) > 65535)
-    return fail(DCA_ERR_UNSUPPORTED, "%s: Hq=%d, Hkv=%d beyond the launch grid", fn, Hq, Hkv);
+  const long long cap = (long long)max_blocks * block_rows;
+  if (!kv4_decode_fits(B, Hq, Hkv, D, cap))
+    return fail(DCA_ERR_UNSUPPORTED, "%s: B=%d, Hq=%d and %lld rows beyond the launch grid", fn, B,
+                Hq, cap);
   DCA_CHECK_PTR(q);
   DCA_CHECK_PTR(pool);
   DCA_CHECK_INDEX(t);
   DCA_CHECK_PTR(O);
   DCA_CHECK_INDEX(LSE);
   DCA_CHECK_PTR(workspace);
-  const size_t need = kv4_decode_workspace_bytes(B, Hq, Hkv, D, (long long)max_blocks * block_rows);
+  const size_t need = kv4_decode_workspace_bytes(B, Hq, Hkv, D, cap);
   if (ws_bytes < need)
     return fail(DCA_ERR_WORKSPACE, "%s: workspace %zu bytes < required %zu", fn, ws_bytes, need);
   const float sc = scale != 0.f ? scale : 1.0f / sqrtf((float)D);

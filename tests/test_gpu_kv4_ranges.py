@@ -181,3 +181,21 @@ def test_decode_of_the_largest_queries_over_keys_of_zero(D, G, rows):
     pool[..., :32 * D + 256 * (D // 64)] = 0  # codes and parameters of the keys
     got = _decode(q, pool, table, t, s, c, rows)
     _close(got, ko.decode(ku.f64(q), pool, table, t, s, c))
+
+
+@pytest.mark.parametrize("rows", ROWS)
+def test_decode_of_very_many_query_heads(rows):
+    # more groups of eight heads on a kv head than a launch's second dimension counts
+    rng, gen = np.random.default_rng(47), torch.Generator().manual_seed(47)
+    D, R, s, c, Hq, part = 64, 64, 40, 60, 70001 * 8, 2000 * 8
+    table, num = ku.random_tables(rng, [41], R)
+    pool = ku.random_pool(rng, num, 1, R, D)
+    q = torch.randn(1, Hq, D, generator=gen).to(torch.bfloat16)
+    O, LSE = _decode(q, pool, table, [40], s, c, rows)
+    for h in (0, 30000 * 8, 65535 * 8 - 1000, Hq - part):  # every unit of a call is worked alike
+        a, b = _decode(q[:, h:h + part].contiguous(), pool, table, [40], s, c, rows)
+        assert torch.equal(O[:, h:h + part], a) and torch.equal(LSE[:, h:h + part], b), h
+    for h in (0, Hq - 24):
+        few = slice(h, h + 24)
+        _close((O[:, few], LSE[:, few]),
+               ko.decode(ku.f64(q[:, few]), pool, table, [40], s, c), h)
