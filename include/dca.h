@@ -408,7 +408,8 @@ size_t dca_attn_decode_workspace(int B, int Hq, int D, int Tcap);
 /* DCA decode of one new token per sequence.  q [B][Hq][D] is the UNROTATED
  * query at absolute index t[b]; Kcache holds keys ALREADY rotated at j mod s
  * (e.g. by dca_rope_rotate with DCA_POS_KEY); keys and values 0 .. t[b] are
- * valid (the new token's own K/V included).  Writes O [B][Hq][D] bf16 and
+ * valid (the new token's own K/V included), rows past t[b] may hold anything.
+ * Writes O [B][Hq][D] bf16 and
  * LSE [B][Hq] fp32.  Split-KV across SMs then an LSE merge (Guide,
  * "Strategic Recommendations", item 3: pair DCA with FlashDecoding).
  * t lives on the device; a t[b] outside [0, Tcap) is reported by

@@ -60,6 +60,17 @@ __device__ __forceinline__ uint32_t dec_off(int r, int ch) {
   return (uint32_t)((ch >> 3) * kBoxBytes + r * 128 + (((ch & 7) ^ (r & 7)) << 4));
 }
 
+// Values of tile rows r0 .. r1 - 1 to 0, by a warp: rows past the sequence hold
+// anything, and their weight of 0 would not clear an infinity or a NaN.  (The last
+// tile of a split: no copy follows into it.)
+template <int D>
+__device__ __noinline__ void clear_rows(uint8_t* values, int r0, int r1, int lane) {
+  for (int i = r0 * (D / 8) + lane; i < r1 * (D / 8); i += 32)
+    *reinterpret_cast<uint4*>(values + dec_off(i / (D / 8), i % (D / 8))) =
+        make_uint4(0, 0, 0, 0);
+  __syncwarp();
+}
+
 template <int D>
 __global__ void __launch_bounds__(kDecThreads) decode_split_kernel(
     const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
@@ -191,6 +202,8 @@ __global__ void __launch_bounds__(kDecThreads) decode_split_kernel(
       const uint32_t vbase = kbase + SM::kHalves * kBoxBytes;
       const int j0 = k_begin + it * kDecKeys + warp * 16;
       if (j0 < k_end) {
+        if (j0 + 16 > k_end)
+          clear_rows<D>(smem + (vbase - ring), warp * 16 + k_end - j0, warp * 16 + 16, lane);
         const int dlo = ci - min(j0 + 15, k_end - 1) / s, dhi = ci - j0 / s;
         float sacc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
