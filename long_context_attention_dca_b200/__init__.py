@@ -627,8 +627,8 @@ def dca_kv4_append_paged(k_new, v_new, pool, block_table, cu_seqlens, t0, s, c, 
 
 def dca_kv4_read_paged(pool, block_table, cu_seqlens, t0, T, D, K=None, V=None):
     """Rows of a paged 4-bit cache as bf16: (K, V) [T, Hkv, D], sequence b's
-    positions t0[b], t0[b]+1, .. at rows cu_seqlens[b] .. cu_seqlens[b+1]-1.
-    With K, V [B, rows, Hkv, D] given, position p goes to row p of entry b."""
+    positions t0[b], t0[b]+1, .. at rows cu_seqlens[b] .. cu_seqlens[b+1]-1
+    (rows of no sequence are left as allocated).  With K, V [B, rows, Hkv, D] given, position p goes to row p of entry b."""
     num_blocks, Hkv, block_rows = _kv4_pool(pool, D)
     B, max_blocks = _kv4_rows(cu_seqlens, t0, block_table)
     if (K is None) != (V is None):

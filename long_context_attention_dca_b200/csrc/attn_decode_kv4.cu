@@ -31,15 +31,17 @@
 // second kernel.
 //
 // What bounds it.  A key costs 144 bytes of cache a kv head (D = 128) and, with
-// eight query heads on it, about 18 instructions a warp (1145 for 64 keys, 96 of
+// eight query heads on it, about 18 instructions a warp (1148 for 64 keys, 96 of
 // them matrix products, half of the rest unpacking nibbles).  With one query
-// head memory bounds it: 24 sequences of 16k keys, 32 kv heads, take 293 us,
-// 6.0 TB/s, 92 % of the copy rate.  With eight, the instructions do: 16 sequences
-// of 33k to 65k keys, 8 kv heads, take 205 us, 4.4 TB/s, where the loads alone
-// take 143; the logic pipe is busy for half of it and the matrix pipe for 37 %,
-// the rest is fixed latency between them.  One sequence of 100k keys takes 42 us
-// against 17.6 of bytes: 9 us pass before the first and after the last tile, and
-// seven or eight tiles a warp follow.
+// head memory bounds it: 24 sequences of 16k keys, 32 kv heads, take 317 us, 5.6
+// TB/s, 85 % of the copy rate.  With eight no pipe is full: 16 sequences of 33k to
+// 65k keys, 8 kv heads, take 203 to 206 us at 1965 MHz, 4.4 TB/s, the logic pipe
+// busy for 51 % and the matrix pipe for 37 % of it, an instruction issued in 0.55 of
+// the cycles; at 2.7 warps a scheduler the latency between dependent instructions
+// is what remains.  (One call after another takes 222 us: the power cap then holds
+// the clock near 1760 MHz.)  One sequence of 100k keys takes 38 us in a graph, 43
+// with a cold cache, against 17.6 of bytes: about 9 us pass before the first and
+// after the last tile, and seven or eight tiles a warp follow.
 #include <atomic>
 
 #include "dca_common.cuh"
@@ -52,14 +54,17 @@ namespace kv4 {
 
 constexpr int kHeads = 8;   // query heads per CTA (MMA N)
 // Three CTAs of four warps an SM, a ring of three half tiles (K or V part) a
-// warp: 64.5 us for 24 x 4k keys of 32 kv heads, 50 for 1 x 100k and 202 for 16 x
-// 64k of 8.  Two CTAs with rings of four took 66, 46 and 208, two of six warps 69,
-// 47 and 212, one of twelve 87, 48 and 235.
+// warp, caches cold: 64.5 us for 24 x 4k keys of 32 kv heads, 44 for 1 x 100k and 206
+// for 16 x 64k of 8.  Two CTAs with rings of four take 66.5, 44 and 208, two of six
+// warps 68, 48 and 218, one of twelve 101, 48 and 241.  The 168 registers that this
+// leaves a thread make the compiler spill at D = 128: 100 bytes a thread with
+// eight query heads a kv head (20 with at most four), 284 (64) in the form that
+// takes units whole.
 constexpr int kWarps = 4;
 constexpr int kRing = 3;
 constexpr int kCtasPerSm = 3;
-constexpr int kMany = 2;    // 16-key steps whose score products run interleaved: 208 us with one
-                            // for the last of those, 204 with two
+constexpr int kMany = 2;    // 16-key steps whose score products run interleaved: with one, 46 and
+                            // 210 us for the last two of those
 constexpr int kMaxTiles = 512;  // of a CTA's share, so that their places fit in shared memory
 
 // Work.  A unit is a (sequence, kv head, group of <= 8 query heads).  The tiles
@@ -74,15 +79,22 @@ constexpr int kMaxTiles = 512;  // of a CTA's share, so that their places fit in
 // at most 1.4 % in the mean, 8 the fastest.
 constexpr int kSetup = 8;
 // Where the caches are short, a unit is not cut: a CTA takes it whole, writes its
-// outputs, and there is nothing to merge.  Against equal shares, in a graph: 64 to
-// 148 units of 100 / 500 / 1000 / 2000 keys, 8 query heads, 9.1 / 9.5 / 12.0 / 16.9
-// us against 12.8 / 16.9 / 19.6 / 22.8; 512 units 20.5 / 24.7 / 33.5 / 52.5 against
-// 22.3 / 28.3 / 37.8 / 54.5, and slower from 3000 keys on; 8 units 8.7 / 9.2 / 11.6 /
-// 16.4 against 10.5 / 10.9 / 10.2 / 10.4, where one launch fewer also saves 2 us
-// of the host's time, which is what such a call waits for outside a graph (962
-// keys, 8 heads: 15.7 us a call against 17.8).
-constexpr int kWide = 8;  // warps of such a CTA where every unit has an SM to itself: 1000 keys
-                          // take 12.0 us, 13.8 with twelve, 14.6 with four
+// outputs, and there is nothing to merge.  In a graph, against equal shares, 8 query
+// heads a unit:
+//     keys      8 units        32             63             128            512
+//      250   7.7 /  9.6    7.9 / 10.2    8.1 / 12.3    8.5 / 15.0   20.4 / 29.6 us
+//      500   8.5 /  9.9    8.6 / 10.5    8.6 / 12.8    8.9 / 17.1   24.9 / 33.7
+//     1000  11.2 / 10.1   11.5 / 11.9   11.4 / 15.9   11.6 / 20.6   35.4 / 42.5
+//     2000       -              -        16.1 / 19.0  16.3 / 24.4   57.9 / 58.7
+//     3000       -              -        21.2 / 20.6  21.5 / 28.9   79.2 / 73.6
+// (63 units: 64 from 2000 keys on.)  Below 48 units shares are faster from 750 keys
+// on, by 1.5 us at most up to 1024 rows; but one launch fewer saves 2.6 us of the
+// host's time at every count of units (15.7 against 18.4 us a call), which is what
+// so short a call waits for outside a graph.  The choice goes by the table's width,
+// which the host knows, not by the lengths, which lie on the device: a short
+// sequence in a wide table takes the shares' time.
+constexpr int kWide = 8;  // warps of such a CTA where every unit has an SM to itself: 148 units of
+                          // 1000 keys take 11.6 us, 13.2 with twelve, 15.2 with four
 constexpr long long kWholeUnits = 0x7FFFFFFF;  // the launch grid
 inline bool takes_whole(long long units, long long cap) {  // cap: rows of a cache
   return units <= kWholeUnits && cap <= (units < 64 ? 1024 : 2048);
@@ -250,7 +262,7 @@ __device__ __forceinline__ void pv(float (&o)[D / 16][kOut], const uint32_t (&wg
 }
 
 // kFew: at most four query heads a kv head.  Eight MMA columns then hold both
-// parts of every query, half the score products: 66 us for 24 x 4k keys of 32 kv
+// parts of every query, half the score products: 64.5 us for 24 x 4k keys of 32 kv
 // heads with a query head each, against 77 as eight columns of high parts.
 template <int D, bool kFew, int W, bool kWhole>
 __global__ void __launch_bounds__(W * 32, W == kWarps ? kCtasPerSm : 1) decode_kernel(
@@ -952,9 +964,10 @@ cudaError_t launch_decode_t(const void* q, const Pages& pg, const int* t, void* 
       LSE, B, Hq, s, c, scale * 1.4426950408889634f, n_hg, make_theta(D, base));
   e = cudaGetLastError();
   if (e != cudaSuccess || whole_units) return e;
-  // Warps by the partials a unit has on average.  With few, a warp a head: 62
-  // sequences of 100 keys with 128 heads take 10 us, against 37 as 7936 blocks of
-  // a head each.  With many, a block a head (one sequence of 100k keys, 64 heads).
+  // Warps by the partials a unit has on average.  A block a head against a warp a
+  // head, 8 heads a unit, in a graph: 4 / 64 / 128 / 440 units of 4000 keys 11.0 / 23.8 /
+  // 34.5 / 91.6 us against 13.7 / 24.2 / 33.2 / 78.8, of 16000 keys 13.4 / 46.3 / 81.4 /
+  // 242 against 27.1 / 46.8 / 79.5 / 236.  They meet where a unit has four to eight.
   auto merge = shares > 4 * units ? decode_merge<D, 1> : decode_merge<D, 8>;
   const int rows = shares > 4 * units ? 1 : 8;
   return launch_early(merge, dim3((Hq + rows - 1) / rows, B), kMergeThreads, stream,

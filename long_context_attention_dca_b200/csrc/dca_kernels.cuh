@@ -7,6 +7,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "../../include/dca.h"
+
 namespace dca {
 
 enum PosRule : int { kPosKey = 0, kPosQIntra = 1, kPosQSucc = 2, kPosQInter = 3, kPosAbsolute = 4 };

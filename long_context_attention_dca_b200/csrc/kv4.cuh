@@ -17,9 +17,11 @@
 //     V codes   [4][D/64][8 words][16 keys]           transposed per 16 keys
 //     V params  [64 keys][D/64]
 // Word i of a group holds its dims 8i .. 8i+7, lowest nibble first; a word
-// belongs to one token, so an append writes whole words.  The two orders make
-// every shared-memory read of the decode kernel a conflict-free 16-byte load
-// of exactly the lane's own MMA fragments.
+// belongs to one token, so an append writes whole words.  In these orders the
+// decode kernel reads nothing but a lane's own MMA fragments from shared memory:
+// values in 16-byte loads without conflicts; keys in 8-byte loads, a group at a
+// time, two lanes of a half warp to a bank (rows 0 and 4, 1 and 5 of each eight lie
+// a multiple of 128 bytes apart); parameters in 4-byte loads without conflicts.
 // A page is [Hkv][block_rows / 64] tiles.
 #pragma once
 

@@ -16,12 +16,16 @@
 // half, and its eight angles serve all kv heads the thread walks.
 //
 // What bounds it: instructions, not memory.  34816 rows of 8 heads of 128 (182 MB
-// in and out, 28 us at the copy rate) take 72 us, with an instruction issued in
-// 0.68 of the cycles: about 770 a warp for 4 rows of K and V, 24 a value, of which
-// a third each go to the rotation with its border checks and to the quantiser.
-// Packed pairs of fp32 (two elements an instruction) and the fp64 path behind
-// a test are what brought it there from 226 us.  Reading back is bound by
-// memory: the same rows take 37 us, 4.9 TB/s.
+// in and out, 28 us at the copy rate) take 74 us, with an instruction issued in
+// 0.69 of the cycles: about 775 a warp for 4 rows of K and V, 24 a value.  Of the
+// 74, the tests of the rotation's roundings cost 2, those of the codes 8, both 12, and
+// the second part of the angles 2 more (timed without each, results then not
+// exact); loads, stores and the groups' ranges alone take 34.  What is left, some 26
+// us, is the arithmetic of the rotation and of the quantiser itself.  Packed pairs
+// of fp32 (two elements an instruction) and the fp64 path behind a test are what
+// brought it there from 226 us.  Reading back the same rows takes 37 us, 4.9 TB/s:
+// the logic pipe, which takes the nibbles apart, is busy for 71 % of it and an
+// instruction is issued in 0.71 of the cycles, so that memory is not alone.
 #include "dca_common.cuh"
 #include "dca_kernels.cuh"
 #include "kv4.cuh"
@@ -30,7 +34,7 @@ namespace dca {
 namespace kv4 {
 
 constexpr int kThreads = 64;  // small blocks fill the last wave: against 128, 23 -> 21 us for
-                              // 3525 rows of 32 heads of 64, 73 -> 72 us for the case above
+                              // 3525 rows of 32 heads of 64, the same for the case above
 
 // A double rounded once to bf16 (nearest even): to fp32 toward zero with the
 // lost bits kept as a sticky last bit, which the second rounding cannot confuse
@@ -395,7 +399,7 @@ __device__ __forceinline__ void dequantise8(uint32_t w, uint32_t param, uint32_t
 // [B][out_rows][Hkv][D].  code * scale + offset is formed in fp32, where it is
 // exact unless the offset is over 2^11 steps away, and rounded once.
 // One block a (run of rows, kv head), so that it reads whole tiles; a thread
-// takes kReadRows rows of the run, all their loads in flight at once (one row: 43 us
+// takes kReadRows rows of the run, all their loads in flight at once (one row: 39 us
 // for the case above; two: 37).
 constexpr int kReadRows = 2;
 

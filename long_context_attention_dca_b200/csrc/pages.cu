@@ -147,9 +147,10 @@ size_t work_ints(int B, int max_blocks, int num_blocks) {
   return list_ints(B, num_blocks) + plan_ints(B, max_blocks, num_blocks);
 }
 // A plan of this many ints or fewer runs in one CTA's shared memory (200 KB).
-// Alone against a cluster in global memory, us (remap / compact): 1037 ints 5.5 /
-// 5.0 against 15.7 / 11.2, 16017 ints 10.3 / 9.2 against 18.6 / 13.2, 38073 ints
-// 17.6 / 15.5 against 20.7 / 14.7.
+// Alone against a cluster in global memory, us (remap / compact): 1037 ints 5.1 /
+// 4.6 against 16.5 / 12.6, 16017 ints 10.0 / 9.1 against 18.1 / 13.2, 38073 ints
+// 17.4 / 15.1 against 21.0 / 14.9: the compaction's two forms meet there, the remap's
+// later.
 constexpr size_t kAloneInts = 50000;
 
 __host__ __device__ inline void carve_plan(Work& w, int* p, int B, int max_blocks,
@@ -550,7 +551,10 @@ __global__ void __cluster_dims__(C, 1, 1) __launch_bounds__(kPlanThreads, 1) com
 // each outer part of a page.  A work item is one chunk of one part; items are
 // numbered over the longest possible copy and the ones past a short copy's end
 // do nothing.  Bound by memory: compacting 975 MB of bf16 pages (1.95 GB in and
-// out) takes 313 us, 6.2 TB/s.
+// out) takes 313 us, 6.2 TB/s.  A block finds its pool by a walk over the list, which
+// shows only where many pools have few pages to copy: a remap with 3 copies in 64
+// bf16 pools (79 MB moved) takes 21 us, plan included, with 64 copies 235 us (1678
+// MB); in 256 pools with 3 copies 124 us (315 MB, 48 us at the copy rate).
 constexpr int kChunk = 32 << 10;
 constexpr int kCopyThreads = 256;
 
